@@ -51,8 +51,8 @@ def listed():
         # weight gradients of eight large experts, fp32
         dict(name="wgrad_large", op="wgrad", fa=E5M2, fb=E4M3, rows=8192, groups=8, m=14336, n=4096, out="f32",
              skew=0.3),
-        # weight gradients of 64 small experts
-        dict(name="wgrad_fine", op="wgrad", fa=E5M2, fb=E4M3, rows=24594, groups=64, m=1408, n=2048, out="f32",
+        # weight gradients of 64 small experts, reduced over the replicas in bf16
+        dict(name="wgrad_fine", op="wgrad", fa=E5M2, fb=E4M3, rows=24594, groups=64, m=1408, n=2048, out="bf16",
              skew=1.0),
         # one token of a generating sequence
         dict(name="layernorm_one", op="layernorm", dtype="bf16", params="bf16", rows=1, cols=4096),
@@ -88,13 +88,12 @@ def draw(rng):
                         fmt=rng.choice([E4M3, E5M2]), columns=rng.choice([True, False]), skew=skew)
         elif op == "gemm":
             case = dict(op=op, fa=rng.choice([E4M3, E5M2]), fb=E4M3, rows=_log(rng, 1, 32768), groups=groups,
-                        n=128 * _log(rng, 4, 112), k=128 * _log(rng, 4, 56), out=rng.choice(["bf16", "bf16", "f32"]),
-                        skew=skew)
+                        n=128 * _log(rng, 4, 112), k=128 * _log(rng, 4, 56), out="bf16", skew=skew)
             if case["groups"] * case["n"] * case["k"] > 8 * 14336 * 4096:
                 continue
         elif op == "wgrad":
             case = dict(op=op, fa=E5M2, fb=E4M3, rows=_log(rng, 64, 32768), groups=groups, m=128 * _log(rng, 4, 112),
-                        n=128 * _log(rng, 4, 56), out=rng.choice(["f32", "f32", "bf16"]), skew=skew)
+                        n=128 * _log(rng, 4, 56), out=rng.choice(["f32", "bf16"]), skew=skew)
             if case["groups"] * case["m"] * case["n"] > 8 * 14336 * 4096:
                 continue
         elif op == "clip":
