@@ -55,6 +55,10 @@ SIGNATURES = {
                                       _VP, _I32, _VP, _VP],
     "fp8_cast_stats": [_VP, _I32, _I64, _I32, _VP, _VP, _VP],
     "fp8_quantize_error_feedback": [_VP, _I32, _VP, _I64, _I32, _VP, _VP, _VP, _VP],
+    "fp8q_layernorm": [_VP, _I32, _I64, _I64, _VP, _VP, _I32, ctypes.c_float, _VP, _VP, _VP, _VP],
+    "fp8q_layernorm_backward": [_VP, _VP, _I32, _I64, _I64, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP],
+    "fp8q_layernorm_backward_workspace": [_I32, _I64, _I64, _VP],
+    "fp8q_grad_norm_clip": [_VP, _VP, _VP, _VP, _I32, ctypes.c_float, _VP, _VP, _VP],
     "fp8q_clock_monitor": [_VP, _VP, _VP],
     "fp8q_set_finish_poll_rounds": [ctypes.c_uint32, _VP],
     "fp8q_last_error": [],
@@ -429,6 +433,92 @@ def fp8_quantize_error_feedback(g, residual, fmt, scale_inv, q, amax_out=None, s
     _check(lib.fp8_quantize_error_feedback(_ptr(g, "g"), _dtype(g), _ptr(residual, "residual"), g.numel(), fmt,
                                            _ptr(scale_inv, "scale_inv"), _ptr(q, "q"), _ptr(amax_out, "amax_out"),
                                            _stream(stream)))
+
+
+def _params(cols, x, **kw):
+    """dtype of the per-column parameters (all of one type); x's when none is given."""
+    got = {n: t for n, t in kw.items() if t is not None}
+    for n, t in got.items():
+        _need(t, n, _HP, cols)
+    types = {t.dtype for t in got.values()}
+    if len(types) > 1:
+        raise TypeError("%s must have one dtype" % " and ".join(sorted(got)))
+    return _dtype(next(iter(got.values()))) if got else _dtype(x)
+
+
+def _same(t, name, x):
+    """t has x's dtype and element count."""
+    _need(t, name, (x.dtype,), x.numel())
+
+
+def _required(**kw):
+    for name, t in kw.items():
+        if t is None:
+            raise ValueError("%s is required" % name)
+
+
+def fp8q_layernorm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
+    """y = layer norm of the rows of x [rows][cols] with gain gamma and bias
+    beta (either may be None); mean, rstd (float32 [rows]) for the backward
+    pass."""
+    rows, cols = _shape2(x)
+    _required(y=y)
+    p_dtype = _params(cols, x, gamma=gamma, beta=beta)
+    _same(y, "y", x)
+    _need(mean, "mean", _F32, rows)
+    _need(rstd, "rstd", _F32, rows)
+    _check(lib.fp8q_layernorm(_ptr(x, "x"), _dtype(x), rows, cols, _ptr(gamma, "gamma"), _ptr(beta, "beta"), p_dtype,
+                              eps, _ptr(y, "y"), _ptr(mean, "mean"), _ptr(rstd, "rstd"), _stream(stream)))
+
+
+def fp8q_layernorm_backward_workspace(dtype, rows, cols):
+    """Bytes of the workspace of fp8q_layernorm_backward (dtype: F32 or BF16)."""
+    n = ctypes.c_int64(0)
+    _check(lib.fp8q_layernorm_backward_workspace(dtype, rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def fp8q_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, workspace=None, stream=None):
+    """dx and (if given) dgamma, dbeta of fp8q_layernorm; workspace: a device
+    tensor of at least fp8q_layernorm_backward_workspace bytes, needed with
+    dgamma or dbeta."""
+    rows, cols = _shape2(x)
+    _required(dy=dy, mean=mean, rstd=rstd, dx=dx)
+    p_dtype = _params(cols, x, gamma=gamma, dgamma=dgamma, dbeta=dbeta)
+    _same(dy, "dy", x)
+    _same(dx, "dx", x)
+    _need(mean, "mean", _F32, rows)
+    _need(rstd, "rstd", _F32, rows)
+    ws_bytes = 0
+    if workspace is not None:
+        _tensor(workspace, "workspace")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.fp8q_layernorm_backward(_ptr(dy, "dy"), _ptr(x, "x"), _dtype(x), rows, cols, _ptr(gamma, "gamma"),
+                                       p_dtype, _ptr(mean, "mean"), _ptr(rstd, "rstd"), _ptr(dx, "dx"),
+                                       _ptr(dgamma, "dgamma"), _ptr(dbeta, "dbeta"), _ptr(workspace, "workspace"),
+                                       ws_bytes, _stream(stream)))
+
+
+def fp8q_grad_norm_clip(grads, max_norm, norm, coef, out=None, stream=None):
+    """norm[0] = the 2-norm over all tensors of grads (float32 / bfloat16, any
+    shapes), coef[0] = min(1, max_norm / (norm + 1e-6)); every gradient is
+    multiplied by coef, in place or into the tensors of out.  An infinite
+    max_norm computes the norm alone."""
+    _required(norm=norm, coef=coef)
+    _scalars(norm=norm, coef=coef)
+    count = len(grads)
+    if out is not None and len(out) != count:
+        raise ValueError("out must have %d tensors, got %d" % (count, len(out)))
+    for i, t in enumerate(grads):
+        _need(t, "grads[%d]" % i, _HP)
+        if out is not None:
+            _same(out[i], "out[%d]" % i, t)
+    g = (_VP * count)(*[_ptr(t, "grads") for t in grads])
+    o = None if out is None else (_VP * count)(*[_ptr(t, "out") for t in out])
+    n = (_I64 * count)(*[t.numel() for t in grads])
+    d = (_I32 * count)(*[_dtype(t) for t in grads])
+    _check(lib.fp8q_grad_norm_clip(g, o, n, d, count, max_norm, _ptr(norm, "norm"), _ptr(coef, "coef"),
+                                   _stream(stream)))
 
 
 CLOCK_BLOCKS = 8

@@ -39,6 +39,11 @@
 // address: the address on the current device comes from hipGetSymbolAddress.
 static __device__ __align__(256) fp8q::GridScratch scratch[fp8q::kScratchSlots];
 
+// The block partials of the gradient norm, kParts sums of squares per slot
+// (overwritten by every call, so they need no clearing): the same slots, a
+// device global of its own.
+static __device__ __align__(256) double square_parts[fp8q::kScratchSlots][fp8q::kParts];
+
 namespace {
 
 thread_local char g_err[512] = "";
@@ -95,6 +100,7 @@ struct DeviceScratch {
     std::once_flag once;
     hipError_t err = hipSuccess;
     fp8q::GridScratch *base = nullptr; // address of `scratch` on this device
+    double *squares = nullptr;         // and of `square_parts`
     Slot slots[fp8q::kScratchSlots];
     std::map<StreamKey, int> slot_of; // guarded by g_table_mu
 };
@@ -115,7 +121,10 @@ public:
         if (dev < 0 || dev >= kMaxDevices) return fail(FP8Q_EUNSUPPORTED, "%s: device %d out of range", fn, dev);
         DeviceScratch &d = g_devices[dev];
         // once per device, with that device current
-        std::call_once(d.once, [&d] { d.err = hipGetSymbolAddress((void **)&d.base, HIP_SYMBOL(scratch)); });
+        std::call_once(d.once, [&d] {
+            d.err = hipGetSymbolAddress((void **)&d.base, HIP_SYMBOL(scratch));
+            if (d.err == hipSuccess) d.err = hipGetSymbolAddress((void **)&d.squares, HIP_SYMBOL(square_parts));
+        });
         if (d.err != hipSuccess) return hip_status(d.err, fn);
         int idx;
         {
@@ -137,6 +146,7 @@ public:
         lock_ = std::unique_lock<std::mutex>(slot_->mu);
         index_ = idx;
         gs = d.base + idx;
+        squares = d.squares + (int64_t)idx * fp8q::kParts;
         if (slot_->dirty) {
             e = fp8q::launch_clear_scratch(gs, s);
             if (e != hipSuccess) return hip_status(e, fn);
@@ -154,6 +164,7 @@ public:
     }
     int index() const { return index_; }
     fp8q::GridScratch *gs = nullptr;
+    double *squares = nullptr;
     uint32_t tag = 0;
 
 private:
@@ -186,6 +197,13 @@ public:
     {
         const int st = lease_.acquire(fn_, (hipStream_t)stream_);
         *gs = st == FP8Q_OK ? lease_.gs : nullptr;
+        return st;
+    }
+    // the slot's partial sums of squares
+    int scratch(double **squares)
+    {
+        const int st = lease_.acquire(fn_, (hipStream_t)stream_);
+        *squares = st == FP8Q_OK ? lease_.squares : nullptr;
         return st;
     }
     // the slot, this call's tag and the polling bound of its finishing block
@@ -918,3 +936,170 @@ extern "C" int fp8_scaled_gemm_fused(const uint8_t *A, int32_t fa, const float *
     return c.ret(fp8_scaled_gemm_fused_impl(c, A, fa, sA, B, fb, sB, M, N, K, mode, bias, act, C, c_type, c_scale_inv, amax_out, stream));
 }
 
+
+// --------------------------------------------------------- layer norm ----
+static int layernorm_shape(const char *fn, int32_t dtype, int64_t rows, int64_t cols)
+{
+    if (!valid_dtype(dtype)) return fail(FP8Q_EINVAL, "%s: unknown dtype", fn);
+    if (rows < 0 || cols < 1) return fail(FP8Q_EINVAL, "%s: rows must be >= 0 and cols >= 1", fn);
+    if (rows > (int64_t)1 << 31 || cols > (int64_t)1 << 31)
+        return fail(FP8Q_EUNSUPPORTED, "%s: a dimension exceeds 2^31", fn);
+    return FP8Q_OK;
+}
+
+static int fp8q_layernorm_impl(const void *x, int32_t dtype, int64_t rows, int64_t cols, const void *gamma,
+                               const void *beta, int32_t p_dtype, float eps, void *y, float *mean, float *rstd,
+                               void *stream)
+{
+    const char *fn = "fp8q_layernorm";
+    const int st = layernorm_shape(fn, dtype, rows, cols);
+    if (st) return st;
+    if (!valid_dtype(p_dtype)) return fail(FP8Q_EINVAL, "%s: unknown dtype", fn);
+    if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(FP8Q_EINVAL, "%s: eps must be finite and not negative", fn);
+    const int64_t e = dsize(dtype), pe = dsize(p_dtype), xb = rows * cols * e, pb = cols * pe;
+    if ((gamma && !aligned(gamma, pe)) || (beta && !aligned(beta, pe)))
+        return fail(FP8Q_EINVAL, "%s: gamma / beta not aligned to their elements", fn);
+    if ((mean && !aligned(mean, 4)) || (rstd && !aligned(rstd, 4)))
+        return fail(FP8Q_EINVAL, "%s: mean / rstd must be 4-byte aligned", fn);
+    if (rows > 0) {
+        if (!x || !aligned(x, e)) return fail(FP8Q_EINVAL, "%s: x must be a pointer aligned to its elements", fn);
+        if (!y || !aligned(y, e)) return fail(FP8Q_EINVAL, "%s: y must be a pointer aligned to its elements", fn);
+        const void *ins[3] = {x, gamma, beta};
+        const int64_t in_b[3] = {xb, gamma ? pb : 0, beta ? pb : 0};
+        void *outs[3] = {y, mean, rstd};
+        const int64_t out_b[3] = {xb, mean ? 4 * rows : 0, rstd ? 4 * rows : 0};
+        for (int o = 0; o < 3; ++o) {
+            for (int i = 0; i < 3; ++i)
+                if (overlap(outs[o], out_b[o], ins[i], in_b[i]))
+                    return fail(FP8Q_EINVAL, "%s: an output overlaps an input", fn);
+            for (int q = 0; q < o; ++q)
+                if (overlap(outs[o], out_b[o], outs[q], out_b[q]))
+                    return fail(FP8Q_EINVAL, "%s: outputs overlap each other", fn);
+        }
+    }
+    return hip_status(fp8q::launch_layernorm(x, dtype, rows, cols, gamma, beta, p_dtype, eps, y, mean, rstd,
+                                             (hipStream_t)stream),
+                      fn);
+}
+
+extern "C" int fp8q_layernorm(const void *x, int32_t dtype, int64_t rows, int64_t cols, const void *gamma,
+                              const void *beta, int32_t p_dtype, float eps, void *y, float *mean, float *rstd,
+                              void *stream)
+{
+    Call c("fp8q_layernorm", stream);
+    c.args("dtype=%lld rows=%lld cols=%lld p_dtype=%lld", (long long)dtype, (long long)rows, (long long)cols, (long long)p_dtype);
+    return c.ret(fp8q_layernorm_impl(x, dtype, rows, cols, gamma, beta, p_dtype, eps, y, mean, rstd, stream));
+}
+
+extern "C" int fp8q_layernorm_backward_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_t *bytes)
+{
+    Call c("fp8q_layernorm_backward_workspace", nullptr);
+    c.args("dtype=%lld rows=%lld cols=%lld", (long long)dtype, (long long)rows, (long long)cols);
+    const int st = layernorm_shape("fp8q_layernorm_backward_workspace", dtype, rows, cols);
+    if (st) return c.ret(st);
+    if (!bytes) return c.ret(fail(FP8Q_EINVAL, "fp8q_layernorm_backward_workspace: bytes must be given"));
+    *bytes = fp8q::layernorm_bwd_workspace(rows, cols, dtype);
+    return c.ret(ok());
+}
+
+static int fp8q_layernorm_backward_impl(const void *dy, const void *x, int32_t dtype, int64_t rows, int64_t cols,
+                                        const void *gamma, int32_t p_dtype, const float *mean, const float *rstd,
+                                        void *dx, void *dgamma, void *dbeta, void *workspace, int64_t workspace_bytes,
+                                        void *stream)
+{
+    const char *fn = "fp8q_layernorm_backward";
+    const int st = layernorm_shape(fn, dtype, rows, cols);
+    if (st) return st;
+    if (!valid_dtype(p_dtype)) return fail(FP8Q_EINVAL, "%s: unknown dtype", fn);
+    const int64_t e = dsize(dtype), pe = dsize(p_dtype), xb = rows * cols * e, pb = cols * pe;
+    if ((gamma && !aligned(gamma, pe)) || (dgamma && !aligned(dgamma, pe)) || (dbeta && !aligned(dbeta, pe)))
+        return fail(FP8Q_EINVAL, "%s: gamma / dgamma / dbeta not aligned to their elements", fn);
+    if (rows > 0) {
+        const void *els[3] = {dy, x, dx};
+        for (const void *p : els)
+            if (!p || !aligned(p, e))
+                return fail(FP8Q_EINVAL, "%s: dy, x and dx must be pointers aligned to their elements", fn);
+        if (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4))
+            return fail(FP8Q_EINVAL, "%s: mean and rstd must be 4-byte aligned pointers", fn);
+    }
+    int64_t need = 0;
+    if (dgamma || dbeta) {
+        need = fp8q::layernorm_bwd_workspace(rows, cols, dtype);
+        if (rows == 0) need = 0;
+        if (need > 0 && (!workspace || !aligned(workspace, 16)))
+            return fail(FP8Q_EINVAL, "%s: workspace must be a 16-byte aligned pointer", fn);
+        if (workspace_bytes < need)
+            return fail(FP8Q_EINVAL, "%s: the workspace needs %lld bytes, got %lld", fn, (long long)need,
+                        (long long)workspace_bytes);
+    }
+    const void *ins[5] = {dy, x, gamma, mean, rstd};
+    const int64_t in_b[5] = {xb, xb, gamma ? pb : 0, 4 * rows, 4 * rows};
+    void *outs[4] = {dx, dgamma, dbeta, workspace};
+    const int64_t out_b[4] = {xb, dgamma ? pb : 0, dbeta ? pb : 0, need};
+    for (int o = 0; o < 4; ++o) {
+        for (int i = 0; i < 5; ++i)
+            if (overlap(outs[o], out_b[o], ins[i], in_b[i]))
+                return fail(FP8Q_EINVAL, "%s: an output overlaps an input", fn);
+        for (int q = 0; q < o; ++q)
+            if (overlap(outs[o], out_b[o], outs[q], out_b[q]))
+                return fail(FP8Q_EINVAL, "%s: outputs overlap each other", fn);
+    }
+    return hip_status(fp8q::launch_layernorm_bwd(dy, x, dtype, rows, cols, gamma, p_dtype, mean, rstd, dx, dgamma,
+                                                 dbeta, (float *)workspace, (hipStream_t)stream),
+                      fn);
+}
+
+extern "C" int fp8q_layernorm_backward(const void *dy, const void *x, int32_t dtype, int64_t rows, int64_t cols,
+                                       const void *gamma, int32_t p_dtype, const float *mean, const float *rstd,
+                                       void *dx, void *dgamma, void *dbeta, void *workspace, int64_t workspace_bytes,
+                                       void *stream)
+{
+    Call c("fp8q_layernorm_backward", stream);
+    c.args("dtype=%lld rows=%lld cols=%lld p_dtype=%lld", (long long)dtype, (long long)rows, (long long)cols, (long long)p_dtype);
+    return c.ret(fp8q_layernorm_backward_impl(dy, x, dtype, rows, cols, gamma, p_dtype, mean, rstd, dx, dgamma, dbeta,
+                                              workspace, workspace_bytes, stream));
+}
+
+// ------------------------------------------------------ gradient norm ----
+static int fp8q_grad_norm_clip_impl(Call &c, const void *const *g, void *const *out, const int64_t *n,
+                                    const int32_t *dtype, int32_t count, float max_norm, float *norm, float *coef,
+                                    void *stream)
+{
+    const char *fn = "fp8q_grad_norm_clip";
+    if (count < 0) return fail(FP8Q_EINVAL, "%s: negative count", fn);
+    if (count > 0 && (!g || !n || !dtype)) return fail(FP8Q_EINVAL, "%s: g, n and dtype must be given", fn);
+    if (!(max_norm >= 0.0f)) return fail(FP8Q_EINVAL, "%s: max_norm must not be negative or NaN", fn);
+    if (!norm || !coef || !aligned(norm, 4) || !aligned(coef, 4) || norm == coef)
+        return fail(FP8Q_EINVAL, "%s: norm and coef must be distinct 4-byte aligned pointers", fn);
+    const bool clip = !(max_norm > 3.4028234e38f); // +inf: the norm only
+    if (!clip && out) return fail(FP8Q_EINVAL, "%s: out must be null with an infinite max_norm", fn);
+    for (int32_t i = 0; i < count; ++i) {
+        if (!valid_dtype(dtype[i])) return fail(FP8Q_EINVAL, "%s: unknown dtype %d of tensor %d", fn, (int)dtype[i], (int)i);
+        if (n[i] < 0 || n[i] > (int64_t)1 << 40)
+            return fail(FP8Q_EINVAL, "%s: tensor %d has a size out of range", fn, (int)i);
+        if (n[i] == 0) continue;
+        const int64_t e = dsize(dtype[i]), b = n[i] * e;
+        if (!g[i] || !aligned(g[i], e)) return fail(FP8Q_EINVAL, "%s: tensor %d not aligned to its elements", fn, (int)i);
+        if (out && (!out[i] || !aligned(out[i], e)))
+            return fail(FP8Q_EINVAL, "%s: output %d not aligned to its elements", fn, (int)i);
+        if (out && out[i] != g[i] && overlap(out[i], b, g[i], b))
+            return fail(FP8Q_EINVAL, "%s: output %d overlaps its gradient", fn, (int)i);
+        const void *w = out ? out[i] : g[i];
+        if (overlap(norm, 4, w, b) || overlap(coef, 4, w, b) || overlap(norm, 4, g[i], b) || overlap(coef, 4, g[i], b))
+            return fail(FP8Q_EINVAL, "%s: norm or coef overlaps tensor %d", fn, (int)i);
+    }
+    double *sq = nullptr;
+    const int st = c.scratch(&sq);
+    if (st) return st;
+    return hip_status(fp8q::launch_grad_norm_clip(g, out, n, dtype, count, max_norm, clip, norm, coef, sq,
+                                                  (hipStream_t)stream),
+                      fn);
+}
+
+extern "C" int fp8q_grad_norm_clip(const void *const *g, void *const *out, const int64_t *n, const int32_t *dtype,
+                                   int32_t count, float max_norm, float *norm, float *coef, void *stream)
+{
+    Call c("fp8q_grad_norm_clip", stream);
+    c.args("count=%lld", (long long)count);
+    return c.ret(fp8q_grad_norm_clip_impl(c, g, out, n, dtype, count, max_norm, norm, coef, stream));
+}

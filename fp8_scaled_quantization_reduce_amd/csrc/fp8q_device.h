@@ -178,6 +178,22 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
+// Wavefront sums by the same steps, every lane gets the result.  The order of
+// the additions is fixed, so equal inputs give equal bits.
+__device__ __forceinline__ float wave_sum_f32(float v)
+{
+#define FP8Q_DPP_ADD(CTRL, ROWS)                                                                                     \
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false))
+    FP8Q_DPP_ADD(0x111, 0xF);
+    FP8Q_DPP_ADD(0x112, 0xF);
+    FP8Q_DPP_ADD(0x114, 0xF);
+    FP8Q_DPP_ADD(0x118, 0xF);
+    FP8Q_DPP_ADD(0x142, 0xA);
+    FP8Q_DPP_ADD(0x143, 0xC);
+#undef FP8Q_DPP_ADD
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
 // Max with the value of lane ^ 16 or lane ^ 32, through gfx950's lane-swap
 // instructions (vector ALU, no LDS round trip): with both operands the same
 // register, v_permlane16_swap leaves each lane its own value in one result

@@ -139,4 +139,19 @@ hipError_t launch_gemm(const uint8_t *A, int fa, const float *sA, const uint8_t 
                        int64_t N, int64_t K, int mode, void *C, int out_kind, const float *bias, int act,
                        const float *out_scale_inv, float *amax_out, GridScratch *gs, hipStream_t s);
 
+// ------------------------------------------------- layer norm, clipping --
+hipError_t launch_layernorm(const void *x, int dtype, int64_t rows, int64_t cols, const void *gamma, const void *beta,
+                            int p_dtype, float eps, void *y, float *mean, float *rstd, hipStream_t s);
+// bytes of the backward pass's partial sums
+int64_t layernorm_bwd_workspace(int64_t rows, int64_t cols, int dtype);
+hipError_t launch_layernorm_bwd(const void *dy, const void *x, int dtype, int64_t rows, int64_t cols,
+                                const void *gamma, int p_dtype, const float *mean, const float *rstd, void *dx,
+                                void *dgamma, void *dbeta, float *ws, hipStream_t s);
+
+// g, out, n, dtype: host arrays of `count`; out null: in place.  sq: kParts
+// partial sums of the stream, overwritten.  clip false: the norm only.
+hipError_t launch_grad_norm_clip(const void *const *g, void *const *out, const int64_t *n, const int32_t *dtype,
+                                 int count, float max_norm, bool clip, float *norm, float *coef, double *sq,
+                                 hipStream_t s);
+
 } // namespace fp8q

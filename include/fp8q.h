@@ -434,6 +434,71 @@ int fp8_quantize_error_feedback(const void *g, int32_t dtype, float *residual, i
                                 const float *scale_inv, uint8_t *q, float *amax_out, void *stream);
 
 /*
+ * fp8q_layernorm -- layer norm of the rows of a matrix, the step before the
+ * casts of a linear layer's input:
+ *   mean = sum_j x_j / cols, var = sum_j (x_j - mean)^2 / cols,
+ *   rstd = 1 / sqrt(var + eps), y_j = (x_j - mean) rstd gamma_j + beta_j
+ * in binary32, y rounded once to its type.
+ *   x, y    [rows][cols] of `dtype` (FP8Q_F32 or FP8Q_BF16); any sizes,
+ *           cols >= 1; aligned to their elements (16 bytes is not needed here
+ *           and in the two calls below)
+ *   gamma, beta (nullable: ones, zeros)  [cols] of `p_dtype`
+ *   eps     finite, not negative
+ *   mean, rstd (nullable)  [rows] floats, for the backward pass
+ * No output may overlap an input (in-place use is not supported) or another
+ * output.
+ */
+int fp8q_layernorm(const void *x, int32_t dtype, int64_t rows, int64_t cols, const void *gamma, const void *beta,
+                   int32_t p_dtype, float eps, void *y, float *mean, float *rstd, void *stream);
+
+/*
+ * fp8q_layernorm_backward -- gradients of fp8q_layernorm: with
+ * xh = (x - mean) rstd and h = dy gamma,
+ *   dx = rstd (h - sum_j h / cols - xh sum_j (h xh) / cols),
+ *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy,
+ * summed in binary32 in a fixed order (equal inputs give equal bits).
+ *   dy, x, dx  [rows][cols] of `dtype`; mean, rstd [rows] of the forward pass
+ *   gamma (nullable: ones) [cols] of `p_dtype`
+ *   dgamma, dbeta (nullable) [cols] of `p_dtype`, overwritten (zeros when
+ *              rows is 0)
+ *   workspace  device memory of at least the bytes that
+ *              fp8q_layernorm_backward_workspace gives for these sizes,
+ *              16-byte aligned, contents free to be overwritten; not needed
+ *              when dgamma and dbeta are both null
+ */
+int fp8q_layernorm_backward(const void *dy, const void *x, int32_t dtype, int64_t rows, int64_t cols,
+                            const void *gamma, int32_t p_dtype, const float *mean, const float *rstd, void *dx,
+                            void *dgamma, void *dbeta, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Writes to the host int64_t *bytes the workspace of fp8q_layernorm_backward
+ * for these sizes.  Enqueues nothing. */
+int fp8q_layernorm_backward_workspace(int32_t dtype, int64_t rows, int64_t cols, int64_t *bytes);
+
+/*
+ * fp8q_grad_norm_clip -- the global norm of a list of gradients and their
+ * clipping by it:
+ *   norm = sqrt(sum over all tensors and elements of g^2),
+ *   coef = min(1, max_norm / (norm + 1e-6)),  out = g coef.
+ * The squares are summed in binary64 in a fixed order; norm and coef are
+ * binary32, each out element is rounded once to its type.  A NaN gradient
+ * gives a NaN norm and coefficient (and so NaN gradients), an infinite one an
+ * infinite norm and the coefficient 0.
+ *   g      HOST array of `count` device pointers; tensor i has n[i] >= 0
+ *          elements of dtype[i] (host arrays too), aligned to its elements
+ *   out    HOST array of device pointers of the same sizes and types, each
+ *          equal to g[i] or not overlapping it; NULL: in place
+ *   max_norm  not negative; +inf: only norm (and coef = 1) are computed, and
+ *          out must be NULL
+ *   norm, coef  one device float each
+ * The arrays are read before the call returns.  The call enqueues two
+ * launches for up to 128 tensors (and two more for every further 128).  Its
+ * block partials are 1024 doubles per stream slot in a device global of their
+ * own, next to the reduction scratch, under the same rules.
+ */
+int fp8q_grad_norm_clip(const void *const *g, void *const *out, const int64_t *n, const int32_t *dtype, int32_t count,
+                        float max_norm, float *norm, float *coef, void *stream);
+
+/*
  * fp8q_clock_monitor -- a measurement aid, not a step of the method: the
  * graphics clock that other work runs at.  Enqueues on `stream` one kernel of
  * 8 one-wave blocks (consecutive blocks start on consecutive XCDs; each needs
