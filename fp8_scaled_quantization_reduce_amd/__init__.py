@@ -55,6 +55,9 @@ SIGNATURES = {
                                       _VP, _I32, _VP, _VP],
     "fp8_cast_stats": [_VP, _I32, _I64, _I32, _VP, _VP, _VP],
     "fp8_quantize_error_feedback": [_VP, _I32, _VP, _I64, _I32, _VP, _VP, _VP, _VP],
+    "fp8_quantize_grouped": [_VP, _I32, _I64, _I64, _VP, _I64, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _I64, _VP],
+    "fp8_grouped_gemm": [_VP, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _I64, _I64, _I64, _VP, _VP],
+    "fp8_grouped_gemm_wgrad": [_VP, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _I64, _I64, _I64, _I64, _VP, _I32, _VP],
     "fp8q_layernorm": [_VP, _I32, _I64, _I64, _VP, _VP, _I32, ctypes.c_float, _VP, _VP, _VP, _VP],
     "fp8q_layernorm_backward": [_VP, _VP, _I32, _I64, _I64, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP],
     "fp8q_layernorm_backward_workspace": [_I32, _I64, _I64, _VP],
@@ -147,6 +150,8 @@ _HP = (torch.float32, torch.bfloat16)
 _U8 = (torch.uint8,)
 _F32 = (torch.float32,)
 _STATS = (torch.int64, torch.uint64)
+_I32T = (torch.int32,)
+_BF16T = (torch.bfloat16,)
 
 
 def _dtype(t) -> int:
@@ -433,6 +438,86 @@ def fp8_quantize_error_feedback(g, residual, fmt, scale_inv, q, amax_out=None, s
     _check(lib.fp8_quantize_error_feedback(_ptr(g, "g"), _dtype(g), _ptr(residual, "residual"), g.numel(), fmt,
                                            _ptr(scale_inv, "scale_inv"), _ptr(q, "q"), _ptr(amax_out, "amax_out"),
                                            _stream(stream)))
+
+
+def _groups(offsets):
+    """Number of groups of an int32 offsets tensor [groups + 1]."""
+    _required(offsets=offsets)
+    _need(offsets, "offsets", _I32T)
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets must be [groups + 1], got shape %s" % (tuple(offsets.shape),))
+    return offsets.numel() - 1
+
+
+def _col_copy(q, s, name, rows):
+    """col_stride of a columnwise copy: codes [rows][col_stride], scales [rows][col_stride/128]."""
+    _need(q, "q_" + name if name == "col" else name, _U8)
+    if q.dim() != 2 or q.shape[0] != rows:
+        raise ValueError("%s must be [%d][col_stride], got shape %s" % ("q_" + name if name == "col" else name, rows,
+                                                                       tuple(q.shape)))
+    _need(s, "s_" + name if name == "col" else "s" + name, _F32, rows * (q.shape[1] // 128))
+    return q.shape[1]
+
+
+def fp8_quantize_grouped(x, offsets, fmt, *, row_index=None, q_row=None, s_row=None, q_col=None, s_col=None,
+                         stream=None):
+    """1x128 block quantization of the rows of x in group order (row t is
+    x[row_index[t]], or x[t]); offsets: int32 [groups + 1] on the device.
+    q_col [cols][col_stride], s_col [cols][col_stride/128]: the columnwise copy
+    with every group padded to whole blocks of 128."""
+    x_rows, cols = _shape2(x)
+    groups = _groups(offsets)
+    _need(row_index, "row_index", _I32T)
+    rows = x_rows if row_index is None else row_index.numel()
+    _need(q_row, "q_row", _U8, rows * cols)
+    _need(s_row, "s_row", _F32, rows * (cols // 128))
+    stride = 0
+    if q_col is not None:
+        _required(s_col=s_col)
+        stride = _col_copy(q_col, s_col, "col", cols)
+    _check(lib.fp8_quantize_grouped(_ptr(x, "x"), _dtype(x), x_rows, cols, _ptr(row_index, "row_index"), rows,
+                                    _ptr(offsets, "offsets"), groups, fmt, _ptr(q_row, "q_row"), _ptr(s_row, "s_row"),
+                                    _ptr(q_col, "q_col"), _ptr(s_col, "s_col"), stride, _stream(stream)))
+
+
+def fp8_grouped_gemm(A, fa, sA, B, fb, sB, offsets, C, stream=None):
+    """C[t] = (A[t]*sA[t]) (B[e]*sB[e])^T for the rows t of group e: A [rows][K],
+    B [groups][N][K] codes, C [rows][N] bfloat16."""
+    groups = _groups(offsets)
+    _required(A=A, sA=sA, B=B, sB=sB, C=C)
+    _need(A, "A", _U8)
+    _need(B, "B", _U8)
+    _need(C, "C", _BF16T)
+    if A.dim() != 2 or B.dim() != 3 or C.dim() != 2:
+        raise ValueError("A and C must be 2-D and B 3-D")
+    rows, K = A.shape
+    N = B.shape[1]
+    if B.shape[0] != groups or B.shape[2] != K or tuple(C.shape) != (rows, N):
+        raise ValueError("shape mismatch: A %s, B %s, C %s, %d groups" % (tuple(A.shape), tuple(B.shape),
+                                                                         tuple(C.shape), groups))
+    _need(sA, "sA", _F32, rows * (K // 128))
+    _need(sB, "sB", _F32, groups * (N // 128) * (K // 128))
+    _check(lib.fp8_grouped_gemm(_ptr(A, "A"), fa, _ptr(sA, "sA"), _ptr(B, "B"), fb, _ptr(sB, "sB"),
+                                _ptr(offsets, "offsets"), groups, rows, N, K, _ptr(C, "C"), _stream(stream)))
+
+
+def fp8_grouped_gemm_wgrad(A, fa, sA, B, fb, sB, offsets, C, stream=None):
+    """C[e] = (A_e*sA_e) (B_e*sB_e)^T over the tokens of group e: A
+    [M][col_stride], B [N][col_stride] columnwise codes of fp8_quantize_grouped,
+    C [groups][M][N] bfloat16 or float32."""
+    groups = _groups(offsets)
+    _required(A=A, sA=sA, B=B, sB=sB, C=C)
+    _need(C, "C", _HP)
+    if C.dim() != 3 or C.shape[0] != groups:
+        raise ValueError("C must be [%d][M][N], got shape %s" % (groups, tuple(C.shape)))
+    M, N = C.shape[1:]
+    stride = _col_copy(A, sA, "A", M)
+    if _col_copy(B, sB, "B", N) != stride:
+        raise ValueError("A and B must have one col_stride")
+    # the tokens in the groups are at most the columns that hold them
+    _check(lib.fp8_grouped_gemm_wgrad(_ptr(A, "A"), fa, _ptr(sA, "sA"), _ptr(B, "B"), fb, _ptr(sB, "sB"),
+                                      _ptr(offsets, "offsets"), groups, stride, stride, M, N, _ptr(C, "C"), _dtype(C),
+                                      _stream(stream)))
 
 
 def _params(cols, x, **kw):

@@ -1103,3 +1103,156 @@ extern "C" int fp8q_grad_norm_clip(const void *const *g, void *const *out, const
     c.args("count=%lld", (long long)count);
     return c.ret(fp8q_grad_norm_clip_impl(c, g, out, n, dtype, count, max_norm, norm, coef, stream));
 }
+
+// -------------------------------------------------------- ragged groups ----
+// Checks of the groups shared by the grouped calls.
+static int check_groups(const char *fn, const int32_t *offsets, int32_t groups, int64_t rows)
+{
+    if (groups < 0 || rows < 0) return fail(FP8Q_EINVAL, "%s: negative groups or rows", fn);
+    if (groups > 1 << 16) return fail(FP8Q_EUNSUPPORTED, "%s: more than 65536 groups", fn);
+    if (rows > 0x7FFFFFFF - 128 * (int64_t)groups)
+        return fail(FP8Q_EUNSUPPORTED, "%s: rows and groups exceed 2^31 padded rows", fn);
+    if (groups > 0 && (!offsets || !aligned(offsets, 4)))
+        return fail(FP8Q_EINVAL, "%s: offsets must be a 4-byte aligned pointer", fn);
+    return FP8Q_OK;
+}
+
+static int fp8_quantize_grouped_impl(const void *x, int32_t dtype, int64_t x_rows, int64_t cols,
+                                     const int32_t *row_index, int64_t rows, const int32_t *offsets, int32_t groups,
+                                     int32_t fmt, uint8_t *q_row, float *s_row, uint8_t *q_col, float *s_col,
+                                     int64_t col_stride, void *stream)
+{
+    const char *fn = "fp8_quantize_grouped";
+    if (!valid_dtype(dtype)) return fail(FP8Q_EINVAL, "%s: unknown dtype %d", fn, (int)dtype);
+    if (!valid_fmt(fmt)) return fail(FP8Q_EINVAL, "%s: unknown format %d", fn, (int)fmt);
+    const int st = check_groups(fn, offsets, groups, rows);
+    if (st) return st;
+    if (x_rows < 0 || cols < 0) return fail(FP8Q_EINVAL, "%s: negative shape", fn);
+    if (cols % 128) return fail(FP8Q_EUNSUPPORTED, "%s: cols must be a multiple of 128", fn);
+    if (x_rows > (int64_t)1 << 31 || cols > (int64_t)1 << 24)
+        return fail(FP8Q_EUNSUPPORTED, "%s: x_rows exceeds 2^31 or cols 2^24", fn);
+    if (!row_index && rows != x_rows) return fail(FP8Q_EINVAL, "%s: rows must equal x_rows without a row_index", fn);
+    if (row_index && !aligned(row_index, 4)) return fail(FP8Q_EINVAL, "%s: row_index must be 4-byte aligned", fn);
+    if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr))
+        return fail(FP8Q_EINVAL, "%s: codes and scales of a copy go together", fn);
+    if (!q_row && !q_col) return fail(FP8Q_EINVAL, "%s: at least one of q_row / q_col is needed", fn);
+    if (q_col && (col_stride < 0 || col_stride % 128))
+        return fail(FP8Q_EINVAL, "%s: col_stride must be a multiple of 128", fn);
+    if (!q_col) col_stride = 0;
+    if (rows > 0 && cols > 0) {
+        if ((x_rows > 0 && !x) || !aligned(x, 16)) return fail(FP8Q_EINVAL, "%s: x must be a 16-byte aligned pointer", fn);
+        if (!aligned(q_row, 16) || !aligned(q_col, 16) || !aligned(s_row, 4) || !aligned(s_col, 4))
+            return fail(FP8Q_EINVAL, "%s: codes must be 16-byte and scales 4-byte aligned", fn);
+        const void *ins[3] = {x, row_index, offsets};
+        const int64_t in_b[3] = {x_rows * cols * dsize(dtype), row_index ? 4 * rows : 0, 4 * ((int64_t)groups + 1)};
+        const void *outs[4] = {q_row, s_row, q_col, s_col};
+        const int64_t out_b[4] = {rows * cols, rows * (cols / 128) * 4, cols * col_stride, cols * (col_stride / 128) * 4};
+        for (int o = 0; o < 4; ++o) {
+            for (int i = 0; i < 3; ++i)
+                if (overlap(outs[o], out_b[o], ins[i], in_b[i]))
+                    return fail(FP8Q_EINVAL, "%s: an output overlaps an input", fn);
+            for (int k = 0; k < o; ++k)
+                if (overlap(outs[o], out_b[o], outs[k], out_b[k]))
+                    return fail(FP8Q_EINVAL, "%s: output buffers overlap", fn);
+        }
+        if ((rows / 128 + groups) * (cols / 128) > 0x7FFFFFFF)
+            return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^31 tiles", fn);
+    }
+    return hip_status(fp8q::launch_quantize_grouped(x, dtype, x_rows, cols, row_index, rows, offsets, groups, fmt,
+                                                    q_row, s_row, q_col, s_col, col_stride, (hipStream_t)stream),
+                      fn);
+}
+
+extern "C" int fp8_quantize_grouped(const void *x, int32_t dtype, int64_t x_rows, int64_t cols,
+                                    const int32_t *row_index, int64_t rows, const int32_t *offsets, int32_t groups,
+                                    int32_t fmt, uint8_t *q_row, float *s_row, uint8_t *q_col, float *s_col,
+                                    int64_t col_stride, void *stream)
+{
+    Call c("fp8_quantize_grouped", stream);
+    c.args("dtype=%lld x_rows=%lld cols=%lld rows=%lld groups=%lld fmt=%lld col_stride=%lld", (long long)dtype, (long long)x_rows, (long long)cols, (long long)rows, (long long)groups, (long long)fmt, (long long)col_stride);
+    return c.ret(fp8_quantize_grouped_impl(x, dtype, x_rows, cols, row_index, rows, offsets, groups, fmt, q_row, s_row,
+                                           q_col, s_col, col_stride, stream));
+}
+
+// Operand checks shared by the grouped GEMMs: `in` and `bytes` of A, B, sA,
+// sB, offsets, and of the output C.
+static int check_grouped_operands(const char *fn, int32_t fa, int32_t fb, const void *const (&in)[5],
+                                  const int64_t (&bytes)[5], const void *C, int64_t c_bytes)
+{
+    if (!valid_fmt(fa) || !valid_fmt(fb)) return fail(FP8Q_EINVAL, "%s: unknown operand format", fn);
+    if (c_bytes > 0 && (!C || !aligned(C, 16))) return fail(FP8Q_EINVAL, "%s: C must be a 16-byte aligned pointer", fn);
+    for (int i = 0; i < 4; ++i)
+        if (bytes[i] > 0 && c_bytes > 0 && (!in[i] || !aligned(in[i], i < 2 ? 16 : 4)))
+            return fail(FP8Q_EINVAL, i < 2 ? "%s: A and B must be 16-byte aligned pointers"
+                                           : "%s: sA and sB must be 4-byte aligned pointers", fn);
+    for (int i = 0; i < 5; ++i)
+        if (overlap(C, c_bytes, in[i], bytes[i])) return fail(FP8Q_EINVAL, "%s: C overlaps an input", fn);
+    return FP8Q_OK;
+}
+
+static int fp8_grouped_gemm_impl(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb,
+                                 const float *sB, const int32_t *offsets, int32_t groups, int64_t rows, int64_t N,
+                                 int64_t K, void *C, void *stream)
+{
+    const char *fn = "fp8_grouped_gemm";
+    int st = check_groups(fn, offsets, groups, rows);
+    if (st) return st;
+    if (N < 0 || K < 0) return fail(FP8Q_EINVAL, "%s: negative shape", fn);
+    if (N % 128 || K % 128) return fail(FP8Q_EUNSUPPORTED, "%s: N and K must be multiples of 128", fn);
+    if (K > (int64_t)1 << 22 || N > (int64_t)1 << 24)
+        return fail(FP8Q_EUNSUPPORTED, "%s: K exceeds 2^22 or N 2^24", fn);
+    if ((rows / 16 + groups) * (N / 16) > 0x7FFFFFFF) return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^31 tiles", fn);
+    const void *in[5] = {A, B, sA, sB, offsets};
+    const int64_t bytes[5] = {rows * K, groups * N * K, rows * (K / 128) * 4, groups * (N / 128) * (K / 128) * 4,
+                              4 * ((int64_t)groups + 1)};
+    st = check_grouped_operands(fn, fa, fb, in, bytes, C, groups > 0 ? rows * N * 2 : 0);
+    if (st) return st;
+    return hip_status(fp8q::launch_grouped_gemm(A, fa, sA, B, fb, sB, offsets, groups, rows, N, K, C,
+                                                (hipStream_t)stream),
+                      fn);
+}
+
+extern "C" int fp8_grouped_gemm(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb,
+                                const float *sB, const int32_t *offsets, int32_t groups, int64_t rows, int64_t N,
+                                int64_t K, void *C, void *stream)
+{
+    Call c("fp8_grouped_gemm", stream);
+    c.args("fa=%lld fb=%lld groups=%lld rows=%lld N=%lld K=%lld", (long long)fa, (long long)fb, (long long)groups, (long long)rows, (long long)N, (long long)K);
+    return c.ret(fp8_grouped_gemm_impl(A, fa, sA, B, fb, sB, offsets, groups, rows, N, K, C, stream));
+}
+
+static int fp8_grouped_gemm_wgrad_impl(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb,
+                                       const float *sB, const int32_t *offsets, int32_t groups, int64_t rows,
+                                       int64_t col_stride, int64_t M, int64_t N, void *C, int32_t c_dtype,
+                                       void *stream)
+{
+    const char *fn = "fp8_grouped_gemm_wgrad";
+    int st = check_groups(fn, offsets, groups, rows);
+    if (st) return st;
+    if (!valid_dtype(c_dtype)) return fail(FP8Q_EINVAL, "%s: unknown output dtype %d", fn, (int)c_dtype);
+    if (M < 0 || N < 0) return fail(FP8Q_EINVAL, "%s: negative shape", fn);
+    if (M % 128 || N % 128) return fail(FP8Q_EUNSUPPORTED, "%s: M and N must be multiples of 128", fn);
+    if (col_stride < 0 || col_stride % 128) return fail(FP8Q_EINVAL, "%s: col_stride must be a multiple of 128", fn);
+    if (col_stride > (int64_t)1 << 22 || M > (int64_t)1 << 24 || N > (int64_t)1 << 24)
+        return fail(FP8Q_EUNSUPPORTED, "%s: col_stride exceeds 2^22 or M or N 2^24", fn);
+    if (groups * (M / 64) * (N / 64) > 0x7FFFFFFF) return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^31 tiles", fn);
+    const void *in[5] = {A, B, sA, sB, offsets};
+    const int64_t bytes[5] = {M * col_stride, N * col_stride, M * (col_stride / 128) * 4, N * (col_stride / 128) * 4,
+                              4 * ((int64_t)groups + 1)};
+    st = check_grouped_operands(fn, fa, fb, in, bytes, C, groups * M * N * dsize(c_dtype));
+    if (st) return st;
+    return hip_status(fp8q::launch_grouped_wgrad(A, fa, sA, B, fb, sB, offsets, groups, rows, col_stride, M, N, C,
+                                                 c_dtype, (hipStream_t)stream),
+                      fn);
+}
+
+extern "C" int fp8_grouped_gemm_wgrad(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb,
+                                      const float *sB, const int32_t *offsets, int32_t groups, int64_t rows,
+                                      int64_t col_stride, int64_t M, int64_t N, void *C, int32_t c_dtype,
+                                      void *stream)
+{
+    Call c("fp8_grouped_gemm_wgrad", stream);
+    c.args("fa=%lld fb=%lld groups=%lld rows=%lld col_stride=%lld M=%lld N=%lld c_dtype=%lld", (long long)fa, (long long)fb, (long long)groups, (long long)rows, (long long)col_stride, (long long)M, (long long)N, (long long)c_dtype);
+    return c.ret(fp8_grouped_gemm_wgrad_impl(A, fa, sA, B, fb, sB, offsets, groups, rows, col_stride, M, N, C, c_dtype,
+                                             stream));
+}

@@ -139,6 +139,23 @@ hipError_t launch_gemm(const uint8_t *A, int fa, const float *sA, const uint8_t 
                        int64_t N, int64_t K, int mode, void *C, int out_kind, const float *bias, int act,
                        const float *out_scale_inv, float *amax_out, GridScratch *gs, hipStream_t s);
 
+// Compute units of the current device (0 when it cannot be told).
+int compute_units();
+
+// ---------------------------------------------------------- ragged groups --
+// Rows gathered by `index` (null: as they are), quantized in 1x128 blocks; the
+// columnwise copy (nullable) gives every group whole blocks of 128 columns of
+// its `stride`.
+hipError_t launch_quantize_grouped(const void *x, int dtype, int64_t x_rows, int64_t cols, const int32_t *index,
+                                   int64_t rows, const int32_t *offsets, int groups, int fmt, uint8_t *q_row,
+                                   float *s_row, uint8_t *q_col, float *s_col, int64_t stride, hipStream_t s);
+hipError_t launch_grouped_gemm(const uint8_t *A, int fa, const float *sA, const uint8_t *B, int fb, const float *sB,
+                               const int32_t *offsets, int groups, int64_t rows, int64_t N, int64_t K, void *C,
+                               hipStream_t s);
+hipError_t launch_grouped_wgrad(const uint8_t *A, int fa, const float *sA, const uint8_t *B, int fb, const float *sB,
+                                const int32_t *offsets, int groups, int64_t rows, int64_t stride, int64_t M,
+                                int64_t N, void *C, int c_dtype, hipStream_t s);
+
 // ------------------------------------------------- layer norm, clipping --
 hipError_t launch_layernorm(const void *x, int dtype, int64_t rows, int64_t cols, const void *gamma, const void *beta,
                             int p_dtype, float eps, void *y, float *mean, float *rstd, hipStream_t s);

@@ -434,6 +434,79 @@ int fp8_quantize_error_feedback(const void *g, int32_t dtype, float *residual, i
                                 const float *scale_inv, uint8_t *q, float *amax_out, void *stream);
 
 /*
+ * Ragged groups (the rows that each expert of a layer gets).  The rows of
+ * group e are offsets[e] .. offsets[e + 1] - 1 of a buffer of `rows` rows;
+ * offsets is DEVICE memory, int32 [groups + 1], from 0 and not decreasing,
+ * and its values never reach the host, so no call waits for a router.  A
+ * group may be empty.  Offsets that decrease or leave 0 .. rows are clamped:
+ * what the calls then compute is unspecified, but they stay inside their
+ * buffers.  What belongs to rows of no group (before offsets[0], from
+ * offsets[groups] on) is unspecified in outputs indexed by row.
+ *
+ * fp8_quantize_grouped -- 1x128 block quantization (as fp8_quantize_block
+ * with block_rows 1) of rows gathered in group order:
+ *   row t of the output is row row_index[t] of x (row t itself when row_index
+ *   is NULL; a row of zeros when row_index[t] is outside x).
+ *   x       [x_rows][cols] of `dtype`; cols a multiple of 128
+ *   row_index (nullable) device int32 [rows]; NULL needs rows == x_rows
+ *   q_row   [rows][cols] codes, s_row [rows][cols/128] dequant scales
+ *   q_col, s_col: the columnwise copy for the weight gradient, in which
+ *           every group gets whole blocks of 128 columns: with
+ *           p[e] = sum over groups before e of ceil(size / 128) * 128, column
+ *           p[e] + i of q_col [cols][col_stride] holds row i of group e, the
+ *           rest of its last block zero rows (codes of 0), and s_col
+ *           [cols][col_stride/128] one scale per block.  col_stride is a
+ *           multiple of 128, at least the last group's end (at most
+ *           rows + 127 * min(groups, rows), rounded up to a block); columns past
+ *           it are not written, and groups that do not fit it are left out
+ *           of the columnwise copy.
+ *   Each copy is nullable (codes and scales together), not both.
+ * Errors: FP8Q_EINVAL for unknown enums, a copy without its scales, no copy,
+ * misalignment, overlapping buffers; FP8Q_EUNSUPPORTED for cols not a
+ * multiple of 128, more than 65536 groups or 2^31 rows.
+ */
+int fp8_quantize_grouped(const void *x, int32_t dtype, int64_t x_rows, int64_t cols, const int32_t *row_index,
+                         int64_t rows, const int32_t *offsets, int32_t groups, int32_t fmt, uint8_t *q_row,
+                         float *s_row, uint8_t *q_col, float *s_col, int64_t col_stride, void *stream);
+
+/*
+ * fp8_grouped_gemm -- a block-scaled product per group ([MFP8] section 6, for
+ * the experts of a layer: fprop with A = the tokens and B = the weights,
+ * dgrad with A = dY and B = the weights transposed):
+ *   C[t] = (A[t] * sA[t]) (B_e * sB_e)^T for the rows t of group e
+ *   A  [rows][K] codes of format fa, sA [rows][K/128] (1x128 blocks)
+ *   B  [groups][N][K] codes of format fb, sB [groups][N/128][K/128] (128x128
+ *      blocks, as fp8_quantize_block writes them group by group)
+ *   C  [rows][N] bf16
+ * with the arithmetic of fp8_scaled_gemm(FP8Q_BLOCK_1x128_128x128).  Groups
+ * may have any number of rows; N and K are multiples of 128 (K at most 2^22).
+ */
+int fp8_grouped_gemm(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb, const float *sB,
+                     const int32_t *offsets, int32_t groups, int64_t rows, int64_t N, int64_t K, void *C,
+                     void *stream);
+
+/*
+ * fp8_grouped_gemm_wgrad -- weight gradients of the groups, contracted over
+ * each group's rows ([MFP8] section 6, dW = dY^T X):
+ *   C[e] = (A_e * sA_e) (B_e * sB_e)^T
+ *   A  [M][col_stride], B [N][col_stride] codes of formats fa, fb and sA
+ *      [M][col_stride/128], sB [N][col_stride/128]: the columnwise copies of
+ *      fp8_quantize_grouped for dY [rows][M] and X [rows][N] with the same
+ *      offsets and col_stride
+ *   C  [groups][M][N] of c_dtype (FP8Q_BF16 or FP8Q_F32); zeros for an empty
+ *      group
+ * With c_dtype FP8Q_BF16 the products run on the FP8 matrix instruction, as
+ * in fp8_scaled_gemm(FP8Q_BLOCK_1x128_1x128).  With FP8Q_F32 the codes are
+ * widened to bf16 (exactly) for the bf16 matrix instruction, whose sums are
+ * binary32: the FP8 instruction adds neighbouring products on about 15 bits,
+ * which an fp32 gradient would show (1.1e-5 in the 2-norm).
+ * M and N are multiples of 128, col_stride at most 2^22.
+ */
+int fp8_grouped_gemm_wgrad(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb,
+                           const float *sB, const int32_t *offsets, int32_t groups, int64_t rows, int64_t col_stride,
+                           int64_t M, int64_t N, void *C, int32_t c_dtype, void *stream);
+
+/*
  * fp8q_layernorm -- layer norm of the rows of a matrix, the step before the
  * casts of a linear layer's input:
  *   mean = sum_j x_j / cols, var = sum_j (x_j - mean)^2 / cols,
