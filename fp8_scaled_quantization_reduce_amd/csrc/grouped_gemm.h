@@ -93,9 +93,9 @@ __global__ __launch_bounds__(256) void grouped_rows_kernel(const uint8_t *__rest
     __shared__ v4f sums[4][4][64];
     const int tiles_n = N / 64;
     const int t = blockIdx.x / tiles_n, n0 = (int)(blockIdx.x % tiles_n) * 64;
-    GroupTile gt;
-    int tiles;
-    if (!find_tile<16>(offsets, groups, rows, t, gt, tiles)) return;
+    GroupTiles<16> tiles(offsets, groups, rows);
+    if (t >= tiles.total) return;
+    const GroupTile gt = tiles.find(t);
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int nk = K / 128;
     const int in_group = 16 * gt.tile + r;
@@ -131,22 +131,333 @@ __global__ __launch_bounds__(256) void grouped_rows_kernel(const uint8_t *__rest
     }
 }
 
-// wgrad with 64 x 64 of one group's C per wave.
-template <int FA, int FB, int DC>
-__global__ __launch_bounds__(64) void grouped_wgrad_kernel(const uint8_t *__restrict__ A, const float *__restrict__ sA,
-                                                           const uint8_t *__restrict__ B, const float *__restrict__ sB,
-                                                           const int32_t *__restrict__ offsets, int groups, int rows,
-                                                           int M, int N, int64_t stride, void *__restrict__ C)
+// ---------------------------------------------------------------------------
+// One kTM x kTN tile of C on eight waves, the ping-pong schedule of
+// gemm_bs_pp_kernel for ragged operands: A and B rows past the tile's own are
+// loaded as zeros (the buffer records end there) and never stored, and the
+// contraction may start anywhere in the operands' rows (wgrad).
+//
+// Waves: kTM / 64 row strips x kTN / kWC column strips of 64 x kWC, group X
+// (waves 0-3) the left half of the columns, Y the right half.  256 x 256 tiles
+// have 64 x 128 waves; 128 x 256 and 256 x 128 tiles, for the rows a group
+// leaves over and for the widened products, 64 x 64.
+//
+// kWide (fp32 results): a read phase also widens the fragments it has read to
+// bf16, while the other group's matrix instructions run, and a compute phase
+// chains four bf16 instructions per 16x16 tile and slice.
+struct PPOperand {
+    const uint8_t *base; // first row of the tile, first byte of the contraction
+    int bytes;           // readable from base
+    int pitch;           // bytes of a row
+    const float *s;      // scales of the first row (128x128: block row) and slice
+    int s_bytes, s_pitch; // readable bytes; floats of a row (of blocks)
+};
+
+template <int kTM, int kTN> struct PPShape {
+    static constexpr int kRS = kTM / 64;            // row strips
+    static constexpr int kCS = 8 / kRS;             // column strips
+    static constexpr int kWC = kTN / kCS;           // a wave's columns
+    static constexpr int kQ = kWC / 2, kJT = kQ / 16; // a half's columns and 16-wide column tiles
+    static constexpr int kA = kTM * kBK, kB2 = kTN / 2 * kBK; // code bytes of A, of B's first / second halves
+    static constexpr int oB0 = kA, oB1 = kA + kB2, oSA = kA + 2 * kB2, oSB0 = oSA + 4 * kTM;
+    static constexpr int oSB1 = oSB0 + 4 * 256, kStage = oSB1 + 4 * 128;
+};
+
+template <int FA, int FB, int kTM, int kTN, bool kRowB, bool kWide, int DC>
+__device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, const PPOperand &A, const PPOperand &B, int kblocks,
+                                        int sb_last, void *C, int64_t ldc, int c_rows, int c_cols)
 {
-    constexpr bool kWide = DC == kF32;
-    const int tiles_n = N / 64, tiles_m = M / 64;
-    const int e = blockIdx.x / (tiles_n * tiles_m), tm = blockIdx.x / tiles_n % tiles_m, tn = blockIdx.x % tiles_n;
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    // blocks of 128 tokens before group e and in it
-    int kb0 = 0, kbn = 0;
+    typedef PPShape<kTM, kTN> P;
+    constexpr int kQ = P::kQ, kJT = P::kJT;
+    constexpr int kAL = kTM / 64, kBL = kTN / 128; // loads per wave of A, of a B half
+    constexpr int G1 = kAL + kBL + 1, G2 = kBL + (kRowB ? 1 : 0);
+    constexpr int kVm = G1 + G2; // younger loads allowed at the end of every phase
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool gx = w < 4;
+    const int wm = w % P::kRS, wn = w / P::kRS;
+    const int fr = lane & 15, fg = lane >> 4;
+    const int ap = A.pitch, bp = B.pitch;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)A.base, 0, A.bytes, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)B.base, 0, B.bytes, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void *)A.s, 0, A.s_bytes, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc((void *)B.s, 0, B.s_bytes, kRawBufferWord3);
+    const int swz_lane = ((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) << 4;
+    const int avoff = (lane >> 3) * ap + swz_lane, bvoff = (lane >> 3) * bp + swz_lane;
+    const int savoff = lane * A.s_pitch * 4;
+    const int sb_lrow = 64 * (w % (kTN / 128));
+    const int sb_voff = kRowB ? (((sb_lrow + lane) / kQ) * 2 * kQ + (sb_lrow + lane) % kQ) * B.s_pitch * 4
+                              : min(lane & 1, sb_last) * B.s_pitch * 4;
+
+    auto load_b = [&](uint8_t *dst, int h, int kb) {
+#pragma unroll
+        for (int u = 0; u < kBL; ++u) {
+            const int row = 8 * (w + 8 * u);
+            const int trow = (row / kQ) * 2 * kQ + kQ * h + row % kQ;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(dst + row * kBK), 16, bvoff, trow * bp + kb * kBK,
+                                                     0, 0);
+        }
+    };
+    auto load_g1 = [&](uint8_t *st, int kb) {
+#pragma unroll
+        for (int u = 0; u < kAL; ++u) {
+            const int row = 8 * (w + 8 * u);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(st + row * kBK), 16, avoff, row * ap + kb * kBK,
+                                                     0, 0);
+        }
+        load_b(st + P::oB0, 0, kb);
+        if (w < 4)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(st + P::oSA + 4 * 64 * (w % P::kRS)), 4, savoff,
+                                                     (64 * (w % P::kRS) * A.s_pitch + kb) * 4, 0, 0);
+        else if constexpr (kRowB)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(st + P::oSB0 + 4 * sb_lrow), 4, sb_voff, kb * 4,
+                                                     0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(st + P::oSB0 + 4 * 64 * (w - 4)), 4, sb_voff,
+                                                     kb * 4, 0, 0);
+    };
+    auto load_g2 = [&](uint8_t *st, int kb) {
+        load_b(st + P::oB1, 1, kb);
+        if constexpr (kRowB)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(st + P::oSB1 + 4 * sb_lrow), 4, sb_voff,
+                                                     (kQ * B.s_pitch + kb) * 4, 0, 0);
+    };
+
+    v4f acc[4][2 * kJT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2 * kJT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    v8i a[4], b[kJT];                         // the slice's A fragments, the half's B fragments
+    bf16x8 aw[kWide ? 4 : 1][4], bw[kWide ? kJT : 1][4]; // the same widened
+    float wi[4];
+    v4f sbq[kJT];
+    v4f pr[3]; // results awaiting promotion (tile t in pr[t % 3])
+
+    auto promote = [&](auto hc, int t) {
+        constexpr int h = decltype(hc)::value;
+        const int i = t & 3, jj = t >> 2;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[i][kJT * h + jj][e] =
+                __builtin_fmaf(pr[t % 3][e], kRowB ? wi[i] * sbq[jj][e] : wi[i], acc[i][kJT * h + jj][e]);
+        asm volatile("" : "+v"(acc[i][kJT * h + jj])); // keeps these FMAs in their phase
+    };
+    constexpr int kT = 4 * kJT;
+    auto compute = [&](auto hc) {
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+            if constexpr (kWide) {
+                v4f c{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[t >> 2][s], aw[t & 3][s], c, 0, 0, 0);
+                pr[t % 3] = c;
+            } else {
+                pr[t % 3] = mfma16x16x128<FB, FA>(b[t >> 2], a[t & 3], v4f{0.f, 0.f, 0.f, 0.f});
+            }
+            if (t >= 2) promote(hc, t - 2);
+        }
+        if constexpr (!kWide) {
+#pragma unroll
+            for (int t = 0; t < kT; ++t) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // MFMA
+                if (t >= 2) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); // promotion FMAs
+            }
+        }
+    };
+    auto tail = [&](auto hc) {
+        promote(hc, kT - 2);
+        promote(hc, kT - 1);
+    };
+    auto read_a = [&](const uint8_t *st) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = read_frag(st, wm * 64 + 16 * i + fr, fg);
+    };
+    auto read_b = [&](const uint8_t *st) {
+#pragma unroll
+        for (int jj = 0; jj < kJT; ++jj) b[jj] = read_frag(st, wn * kQ + 16 * jj + fr, fg);
+    };
+    auto widen_a = [&]() {
+        if constexpr (kWide) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) aw[i][s] = widen8<FA>(a[i][2 * s], a[i][2 * s + 1]);
+        }
+    };
+    auto widen_b = [&]() {
+        if constexpr (kWide) {
+#pragma unroll
+            for (int jj = 0; jj < kJT; ++jj)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) bw[jj][s] = widen8<FB>(b[jj][2 * s], b[jj][2 * s + 1]);
+        }
+    };
+    auto read_scales = [&](const uint8_t *st, int off_b, int h) {
+        const float *ssa = reinterpret_cast<const float *>(st + P::oSA);
+        const float *ssb = reinterpret_cast<const float *>(st + off_b);
+        if (h == 0) {
+            // 128x128 blocks: a wave's columns lie in one column block
+            const float sb = kRowB ? 1.0f : ssb[kTN == 256 ? wn * P::kWC / 128 : 0];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float sa = ssa[wm * 64 + 16 * i + fr];
+                wi[i] = kRowB ? sa : sa * sb;
+            }
+        }
+        if constexpr (kRowB) {
+#pragma unroll
+            for (int jj = 0; jj < kJT; ++jj)
+                sbq[jj] = *reinterpret_cast<const v4f *>(ssb + wn * kQ + 16 * jj + 4 * fg);
+        }
+    };
+    auto phase_end = [&](auto wc) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(decltype(wc)::value);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto sync_lds = [&]() { phase_end(PhaseC<waitcnt_imm(kVm, 0)>{}); };
+    auto sync = [&]() { phase_end(PhaseC<waitcnt_imm(kVm, 15)>{}); };
+    using H0 = PhaseC<0>;
+    using H1 = PhaseC<1>;
+
+    auto slice = [&](int kb, uint8_t *cur, uint8_t *nxt) {
+        read_a(cur);
+        read_b(cur + P::oB0);
+        tail(H1{});
+        read_scales(cur, P::oSB0, 0);
+        load_g2(nxt, kb + 1);
+        widen_a();
+        widen_b();
+        sync_lds();
+        compute(H0{});
+        sync();
+        read_b(cur + P::oB1);
+        tail(H0{});
+        read_scales(cur, P::oSB1, 1);
+        load_g1(cur, kb + 2);
+        widen_b();
+        sync_lds();
+        compute(H1{});
+        sync();
+    };
+
+    if (kblocks > 0) {
+        load_g1(st0, 0);
+        load_g2(st0, 0);
+        load_g1(st1, 1);
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(G2 + G1, 15));
+    }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int q = 0; q < 3; ++q) pr[q] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wi[i] = 0.0f;
+#pragma unroll
+    for (int jj = 0; jj < kJT; ++jj) sbq[jj] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (!gx) sync(); // group Y starts one phase later
+    int kb = 0;
+    for (; kb + 1 < kblocks; kb += 2) {
+        slice(kb, st0, st1);
+        slice(kb + 1, st1, st0);
+    }
+    if (kb < kblocks) slice(kb, st0, st1);
+    if (gx) sync(); // and ends one phase later
+    tail(H1{});
+    // the loads of the slices past the end must land before the stages are reused
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+
+    // epilogue: each wave stages its 64 x kWC results and stores whole row pieces
+    constexpr int kB = DC == kF32 ? 4 : 2;
+    typedef EpiStage<P::kWC, kB, 64, P::kWC * kBK> ES;
+    const int wrow = wm * 64, wcol = wn * P::kWC;
+    const bool inside = wrow < c_rows && wcol < c_cols;
+    uint8_t *ep = (w < 4 ? st0 : st1) + (w & 3) * (P::kWC * kBK);
+    uint32_t m = 0;
+    const Epi none{nullptr, kActNone, nullptr};
+#pragma unroll
+    for (int ps = 0; ps < ES::kPasses; ++ps) {
+        if (ps > 0) __syncthreads();
+        if (inside) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((16 * i) / ES::kPassRows != ps) continue;
+#pragma unroll
+                for (int j = 0; j < 2 * kJT; ++j)
+                    ES::put(ep, 16 * i + fr - ps * ES::kPassRows, 4 * j + fg,
+                            pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, acc[i][j], m, none, 0.0f));
+            }
+        }
+        __syncthreads();
+        if (inside) {
+            const int c = lane % ES::kNC, rr = lane / ES::kNC;
+            uint8_t *Cb = reinterpret_cast<uint8_t *>(C);
+#pragma unroll 4
+            for (int s = 0; s < ES::kPassRows / ES::kRowsPerStore; ++s) {
+                const int r = s * ES::kRowsPerStore + rr, row = wrow + ps * ES::kPassRows + r;
+                const uint4 v = *reinterpret_cast<const uint4 *>(ep + ES::addr(r, c));
+                if (row < c_rows) st_stream(Cb + ((int64_t)row * ldc + wcol) * kB + 16 * c, v);
+            }
+        }
+    }
+}
+
+// Block b of a grid -> tile of `n` tiles, each XCD a contiguous run; >= n: none.
+__device__ __forceinline__ int xcd_tile(int b, int n)
+{
+    const int per = (n + kXcds - 1) / kXcds, i = b / kXcds;
+    return i < per ? (b % kXcds) * per + i : n;
+}
+
+// fprop / dgrad in tiles of 256 rows x 256 columns; a group's last tile of at
+// most 128 rows runs as a 128 x 256 tile.
+template <int FA, int FB>
+__global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t *__restrict__ A,
+                                                                   const float *__restrict__ sA,
+                                                                   const uint8_t *__restrict__ B,
+                                                                   const float *__restrict__ sB,
+                                                                   const int32_t *__restrict__ offsets, int groups,
+                                                                   int rows, int N, int K, uint16_t *__restrict__ C)
+{
+    typedef PPShape<256, 256> P;
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[P::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1[P::kStage];
+    const int tiles_n = (N + 255) / 256, nk = K / kBK;
+    GroupTiles<256> tiles(offsets, groups, rows);
+    const int t = xcd_tile(blockIdx.x, tiles.total * tiles_n);
+    if (t >= tiles.total * tiles_n) return;
+    const GroupTile gt = tiles.find(t / tiles_n);
+    int tm, tn;
+    group_tile(gt.tile * tiles_n + t % tiles_n, (gt.size + 255) / 256, tiles_n, tm, tn);
+    const int64_t row0 = gt.row0 + 256 * tm, n0 = 256 * tn;
+    const int a_rows = min(256, gt.size - 256 * tm), b_rows = min(256, N - (int)n0);
+    const PPOperand a{A + row0 * K, a_rows * K, K, sA + row0 * nk, a_rows * nk * 4, nk};
+    const int b_blocks = b_rows / 128; // 1 in a last, half-empty tile column
+    const PPOperand b{B + ((int64_t)gt.group * N + n0) * K, b_rows * K, K,
+                      sB + ((int64_t)gt.group * (N / 128) + n0 / 128) * nk, b_blocks * nk * 4, nk};
+    uint16_t *c = C + row0 * N + n0;
+    if (a_rows > 128)
+        pp_tile<FA, FB, 256, 256, false, false, kBF16>(st0, st1, a, b, nk, b_blocks - 1, c, N, a_rows,
+                                                       b_rows);
+    else
+        pp_tile<FA, FB, 128, 256, false, false, kBF16>(st0, st1, a, b, nk, b_blocks - 1, c, N, a_rows,
+                                                       b_rows);
+}
+
+// Blocks of 128 tokens before group e and in it (wave-uniform).
+__device__ __forceinline__ void group_blocks(const int32_t *offsets, int groups, int rows, int e, int kbs, int &kb0,
+                                             int &kbn)
+{
+    kb0 = kbn = 0;
     for (int g0 = 0; g0 <= e; g0 += 64) {
         int lo, size;
-        group_rows(offsets, groups, rows, g0 + lane, lo, size);
+        group_rows(offsets, groups, rows, g0 + (threadIdx.x & 63), lo, size);
         const int count = (int)(((unsigned)size + 127) / 128), sum = wave_scan_i32(count);
         if (e < g0 + 64) {
             kbn = __builtin_amdgcn_readlane(count, e - g0);
@@ -155,65 +466,62 @@ __global__ __launch_bounds__(64) void grouped_wgrad_kernel(const uint8_t *__rest
             kb0 += __builtin_amdgcn_readlane(sum, 63);
         }
     }
-    const int kbs = (int)(stride / 128);
+    // the caller's buffers may be too short for these offsets
     kb0 = min(kb0, kbs);
     kbn = min(kbn, kbs - kb0);
-    v4f acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int kb = kb0; kb < kb0 + kbn; ++kb) {
-        v8i a[4], b[4];
-        float wa[4];
-        v4f wb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = tm * 64 + 16 * i + r, n = tn * 64 + 16 * i + r;
-            a[i] = load_frag(A + m * stride + (int64_t)kb * 128, g);
-            b[i] = load_frag(B + n * stride + (int64_t)kb * 128, g);
-            wa[i] = sA[m * kbs + kb];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) wb[i][q] = sB[(int64_t)(tn * 64 + 16 * i + 4 * g + q) * kbs + kb];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const v4f p = slice16<FA, FB, kWide>(b[j], a[i]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[q], wa[i] * wb[j][q], acc[i][j][q]);
-            }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t at = ((int64_t)e * M + tm * 64 + 16 * i + r) * N + tn * 64 + 16 * j + 4 * g;
-            if constexpr (DC == kF32) *reinterpret_cast<v4f *>((float *)C + at) = acc[i][j];
-            else
-                *reinterpret_cast<uint2 *>((uint16_t *)C + at) =
-                    __builtin_bit_cast(uint2, __builtin_convertvector(acc[i][j], bf16x4));
-        }
+}
+
+// wgrad in kTM x kTN tiles of one group's C per block.
+template <int FA, int FB, int kTM, int kTN, int DC>
+__global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
+    const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,
+    const float *__restrict__ sB, const int32_t *__restrict__ offsets, int groups, int rows, int M, int N,
+    int64_t stride, void *__restrict__ C)
+{
+    typedef PPShape<kTM, kTN> P;
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[P::kStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1[P::kStage];
+    const int tiles_m = (M + kTM - 1) / kTM, tiles_n = (N + kTN - 1) / kTN, per = tiles_m * tiles_n;
+    const int t = xcd_tile(blockIdx.x, groups * per);
+    if (t >= groups * per) return;
+    const int e = t / per;
+    int tm, tn, kb0, kbn;
+    group_tile(t - e * per, tiles_m, tiles_n, tm, tn);
+    const int kbs = (int)(stride / 128);
+    group_blocks(offsets, groups, rows, e, kbs, kb0, kbn);
+    const int64_t m0 = (int64_t)tm * kTM, n0 = (int64_t)tn * kTN;
+    const int a_rows = min(kTM, M - (int)m0), b_rows = min(kTN, N - (int)n0), pitch = (int)stride;
+    const PPOperand a{A + m0 * stride + (int64_t)kb0 * 128, a_rows * pitch - kb0 * 128, pitch, sA + m0 * kbs + kb0,
+                      (a_rows * kbs - kb0) * 4, kbs};
+    const PPOperand b{B + n0 * stride + (int64_t)kb0 * 128, b_rows * pitch - kb0 * 128, pitch, sB + n0 * kbs + kb0,
+                      (b_rows * kbs - kb0) * 4, kbs};
+    uint8_t *c = reinterpret_cast<uint8_t *>(C) + (((int64_t)e * M + m0) * N + n0) * (DC == kF32 ? 4 : 2);
+    pp_tile<FA, FB, kTM, kTN, true, DC == kF32, DC>(st0, st1, a, b, kbn, 0, c, N, a_rows, b_rows);
 }
 
 template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
 {
-    const unsigned grid = (unsigned)(max_tiles(a.rows, a.groups, 16) * (a.N / 64));
-    grouped_rows_kernel<FA, FB, kBF16><<<grid, 256, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows,
-                                                                   (int)a.N, (int)a.K, a.C);
+    if (a.rows > 16 * a.groups) {
+        const int64_t tiles = max_tiles(a.rows, a.groups, 256) * ((a.N + 255) / 256);
+        grouped_pp_kernel<FA, FB><<<(unsigned)(tiles + kXcds), kBSThreads, 0, a.stream>>>(
+            a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C);
+    } else {
+        const unsigned grid = (unsigned)(max_tiles(a.rows, a.groups, 16) * (a.N / 64));
+        grouped_rows_kernel<FA, FB, kBF16><<<grid, 256, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups,
+                                                                       a.rows, (int)a.N, (int)a.K, a.C);
+    }
     return hipGetLastError();
 }
 
 template <int FA, int FB> hipError_t launch_grouped_wgrad(const GroupedArgs &a)
 {
-    const unsigned grid = (unsigned)((int64_t)a.groups * (a.M / 64) * (a.N / 64));
-    if (a.c_dtype == kF32)
-        grouped_wgrad_kernel<FA, FB, kF32><<<grid, 64, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups,
-                                                                      a.rows, (int)a.M, (int)a.N, a.stride, a.C);
-    else
-        grouped_wgrad_kernel<FA, FB, kBF16><<<grid, 64, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups,
-                                                                       a.rows, (int)a.M, (int)a.N, a.stride, a.C);
+#define FP8Q_WGRAD(TM, TN, DC)                                                                                       \
+    grouped_wgrad_pp_kernel<FA, FB, TM, TN, DC>                                                                      \
+        <<<(unsigned)((int64_t)a.groups * ((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN) + kXcds), kBSThreads, 0,     \
+           a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N, a.stride, a.C)
+    if (a.c_dtype == kBF16) FP8Q_WGRAD(256, 256, kBF16);
+    else FP8Q_WGRAD(256, 128, kF32);
+#undef FP8Q_WGRAD
     return hipGetLastError();
 }
 

@@ -104,9 +104,9 @@ __global__ __launch_bounds__(kGqThreads) void tile_both_kernel(
     __shared__ float colscale[128];
     const int blocks_c = (int)(cols / 128);
     const int t = (int)(blockIdx.x / blocks_c), cb = (int)(blockIdx.x % blocks_c);
-    GroupTile gt;
-    int tiles;
-    if (!find_tile<128>(offsets, groups, rows, t, gt, tiles)) return;
+    GroupTiles<128> tiles(offsets, groups, rows);
+    if (t >= tiles.total) return;
+    const GroupTile gt = tiles.find(t);
     const int ig = threadIdx.x >> 3, jg = threadIdx.x & 7, wave = threadIdx.x >> 6;
     const int64_t c0 = (int64_t)cb * 128 + 16 * jg;
     float v[4][16];

@@ -5,7 +5,7 @@
 // `rows` rows.  The offsets are device data that the host never sees, so a
 // launch covers the most tiles that any offsets could need (max_tiles) and
 // each block looks its tile up: a wave reads 64 groups at a time, counts
-// their tiles and scans the counts.  Offsets are clamped to 0 .. rows and to
+// their tiles and scans the counts (GroupTiles).  Offsets are clamped to 0 .. rows and to
 // not decrease, so whatever they hold, every tile lies inside the buffer.
 //
 // The token-contiguous (columnwise) copies give every group whole blocks of
@@ -46,34 +46,46 @@ __device__ __forceinline__ void group_rows(const int32_t *offsets, int groups, i
     size = min(max(b, lo), rows) - lo;
 }
 
-// The group that holds tile t when every group is cut into tiles of kTile
-// rows (a wave-uniform answer; all 64 lanes must call it).  false: there are
-// not that many tiles; `tiles` is then their number.
-template <int kTile>
-__device__ __forceinline__ bool find_tile(const int32_t *offsets, int groups, int rows, int t, GroupTile &gt,
-                                          int &tiles)
-{
-    const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int g0 = 0; g0 < groups; g0 += 64) {
-        int lo, size;
-        group_rows(offsets, groups, rows, g0 + lane, lo, size);
-        const int count = (int)(((unsigned)size + kTile - 1) / kTile);
-        const int sum = wave_scan_i32(count);
-        const unsigned long long past = __ballot(base + sum > t);
-        if (past) {
-            const int l = __ffsll(past) - 1;
-            gt.group = g0 + l;
-            gt.row0 = __builtin_amdgcn_readlane(lo, l);
-            gt.size = __builtin_amdgcn_readlane(size, l);
-            gt.tile = t - (base + __builtin_amdgcn_readlane(sum - count, l));
-            return true;
-        }
-        base += __builtin_amdgcn_readlane(sum, 63);
+// The groups cut into tiles of kTile rows.  A wave holds 64 groups at a time;
+// with at most 64 the offsets are read once.  All 64 lanes must construct it
+// and call find, whose answers are wave-uniform.
+template <int kTile> struct GroupTiles {
+    const int32_t *offsets;
+    int groups, rows;
+    int lo, size, count, sum; // of group 64 i + lane, for the chunk held
+    int total;                // tiles of all groups
+
+    __device__ __forceinline__ void hold(int g0)
+    {
+        group_rows(offsets, groups, rows, g0 + (threadIdx.x & 63), lo, size);
+        count = (int)(((unsigned)size + kTile - 1) / kTile);
+        sum = wave_scan_i32(count);
     }
-    tiles = base;
-    return false;
-}
+    __device__ __forceinline__ GroupTiles(const int32_t *o, int g, int r) : offsets(o), groups(g), rows(r), total(0)
+    {
+        for (int g0 = 0; g0 < groups; g0 += 64) {
+            hold(g0);
+            total += __builtin_amdgcn_readlane(sum, 63);
+        }
+    }
+    // the group that holds tile t, 0 <= t < total
+    __device__ __forceinline__ GroupTile find(int t)
+    {
+        int base = 0;
+        for (int g0 = 0;; g0 += 64) {
+            if (groups > 64) hold(g0);
+            const int tiles = __builtin_amdgcn_readlane(sum, 63);
+            if (t < base + tiles || g0 + 64 >= groups) {
+                const unsigned long long past = __ballot(base + sum > t);
+                const int l = past ? __ffsll(past) - 1 : 63;
+                const int first = base + __builtin_amdgcn_readlane(sum - count, l);
+                return GroupTile{g0 + l, __builtin_amdgcn_readlane(lo, l), __builtin_amdgcn_readlane(size, l),
+                                 t - first};
+            }
+            base += tiles;
+        }
+    }
+};
 
 // The most tiles of `tile` rows that `groups` groups over `rows` rows can have.
 inline int64_t max_tiles(int64_t rows, int groups, int tile)
