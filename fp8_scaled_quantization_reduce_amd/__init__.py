@@ -15,6 +15,7 @@ E5M2 (1).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -117,7 +118,8 @@ def _need(t, name, dtypes, numel=None, at_least=False):
     at_least, `numel` or more: an input the kernels read a prefix of)."""
     if t is None:
         return
-    _tensor(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous():
+        _tensor(t, name)
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
     if numel is None:
@@ -132,15 +134,22 @@ def _need_scalar(t, name):
     _need(t, name, (torch.float32,), 1)
 
 
+# The current device and stream without torch.cuda's Python layers (2.8 us a
+# call for the stream, against 0.1 us: as long as a small kernel runs).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _ptr(t, name="tensor"):
     """Device address of a contiguous tensor on the current GPU (None -> NULL)."""
     if t is None:
         return None
-    _tensor(t, name)
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous():
+        _tensor(t, name)
     dev = t.get_device()  # -1 for host tensors
     if dev < 0:
         raise ValueError("%s must be a GPU tensor (device %s)" % (name, t.device))
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (name, dev,
                                                                                torch.cuda.current_device()))
     return t.data_ptr()
@@ -164,6 +173,8 @@ def _dtype(t) -> int:
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -584,6 +595,28 @@ def fp8q_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=Non
                                        ws_bytes, _stream(stream)))
 
 
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _tensor_list(ts):
+    """Addresses, element counts and dtype codes of a list of contiguous
+    float32 / bfloat16 tensors on the current GPU, as C arrays; None if it is
+    not one (one C call per tensor and property: the list of a model's
+    gradients is long)."""
+    T = torch.Tensor
+    try:
+        d = array.array("i", [_CODES[t.dtype] for t in ts])
+        if all(map(T.is_contiguous, ts)) and (not len(ts) or set(map(T.get_device, ts)) == {_current_device()}):
+            return array.array("Q", map(T.data_ptr, ts)), array.array("q", map(T.numel, ts)), d
+    except (KeyError, TypeError, AttributeError, RuntimeError):
+        pass
+    return None
+
+
+def _address(a):
+    return a.buffer_info()[0]
+
+
 def fp8q_grad_norm_clip(grads, max_norm, norm, coef, out=None, stream=None):
     """norm[0] = the 2-norm over all tensors of grads (float32 / bfloat16, any
     shapes), coef[0] = min(1, max_norm / (norm + 1e-6)); every gradient is
@@ -594,16 +627,23 @@ def fp8q_grad_norm_clip(grads, max_norm, norm, coef, out=None, stream=None):
     count = len(grads)
     if out is not None and len(out) != count:
         raise ValueError("out must have %d tensors, got %d" % (count, len(out)))
-    for i, t in enumerate(grads):
-        _need(t, "grads[%d]" % i, _HP)
-        if out is not None:
+    g = _tensor_list(grads)
+    o = None if out is None else _tensor_list(out)
+    if g is None or (out is not None and (o is None or o[1:] != g[1:])):
+        # find what is wrong: types and sizes first, the device last
+        for i, t in enumerate(grads):
+            _need(t, "grads[%d]" % i, _HP)
+        for i, t in enumerate(grads if out is not None else ()):
             _same(out[i], "out[%d]" % i, t)
-    g = (_VP * count)(*[_ptr(t, "grads") for t in grads])
-    o = None if out is None else (_VP * count)(*[_ptr(t, "out") for t in out])
-    n = (_I64 * count)(*[t.numel() for t in grads])
-    d = (_I32 * count)(*[_dtype(t) for t in grads])
-    _check(lib.fp8q_grad_norm_clip(g, o, n, d, count, max_norm, _ptr(norm, "norm"), _ptr(coef, "coef"),
-                                   _stream(stream)))
+        for i, t in enumerate(grads):
+            _ptr(t, "grads[%d]" % i)
+        for i, t in enumerate(out or ()):
+            _ptr(t, "out[%d]" % i)
+        raise ValueError("grads and out must be lists of GPU tensors")
+    g, n, d = g
+    # the arrays outlive the call, which reads them before it returns
+    _check(lib.fp8q_grad_norm_clip(_address(g), None if o is None else _address(o[0]), _address(n), _address(d), count,
+                                   max_norm, _ptr(norm, "norm"), _ptr(coef, "coef"), _stream(stream)))
 
 
 CLOCK_BLOCKS = 8

@@ -159,18 +159,22 @@ template <int kTM, int kTN> struct PPShape {
     static constexpr int kWC = kTN / kCS;           // a wave's columns
     static constexpr int kQ = kWC / 2, kJT = kQ / 16; // a half's columns and 16-wide column tiles
     static constexpr int kA = kTM * kBK, kB2 = kTN / 2 * kBK; // code bytes of A, of B's first / second halves
-    static constexpr int oB0 = kA, oB1 = kA + kB2, oSA = kA + 2 * kB2, oSB0 = oSA + 4 * kTM;
-    static constexpr int oSB1 = oSB0 + 4 * 256, kStage = oSB1 + 4 * 128;
+    static constexpr int oB0 = kA, oB1 = kA + kB2, kStage = kA + 2 * kB2;
 };
 
+// Scales of four slices, three groups of them in LDS: a run of 16 rows is 64
+// floats, [slice][row].
+constexpr int kScaleGroups = 3;
+template <int kTM, int kTN, bool kRowB> constexpr int pp_scale_runs() { return kTM / 16 + (kRowB ? kTN / 16 : 1); }
+
 template <int FA, int FB, int kTM, int kTN, bool kRowB, bool kWide, int DC>
-__device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, const PPOperand &A, const PPOperand &B, int kblocks,
+__device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, const PPOperand &A, const PPOperand &B, int kblocks,
                                         int sb_last, void *C, int64_t ldc, int c_rows, int c_cols)
 {
     typedef PPShape<kTM, kTN> P;
     constexpr int kQ = P::kQ, kJT = P::kJT;
     constexpr int kAL = kTM / 64, kBL = kTN / 128; // loads per wave of A, of a B half
-    constexpr int G1 = kAL + kBL + 1, G2 = kBL + (kRowB ? 1 : 0);
+    constexpr int G1 = kAL + kBL, G2 = kBL + 1; // G2 with the slice's load of scales
     constexpr int kVm = G1 + G2; // younger loads allowed at the end of every phase
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -184,10 +188,9 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, const PPOper
     const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc((void *)B.s, 0, B.s_bytes, kRawBufferWord3);
     const int swz_lane = ((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) << 4;
     const int avoff = (lane >> 3) * ap + swz_lane, bvoff = (lane >> 3) * bp + swz_lane;
-    const int savoff = lane * A.s_pitch * 4;
-    const int sb_lrow = 64 * (w % (kTN / 128));
-    const int sb_voff = kRowB ? (((sb_lrow + lane) / kQ) * 2 * kQ + (sb_lrow + lane) % kQ) * B.s_pitch * 4
-                              : min(lane & 1, sb_last) * B.s_pitch * 4;
+    const int sx_row = lane & 15, sx_slice = lane >> 4;
+    const int sa_voff = (sx_row * A.s_pitch + sx_slice) * 4;
+    const int sb_voff = ((kRowB ? sx_row : min(sx_row, sb_last)) * B.s_pitch + sx_slice) * 4;
 
     auto load_b = [&](uint8_t *dst, int h, int kb) {
 #pragma unroll
@@ -206,21 +209,24 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, const PPOper
                                                      0, 0);
         }
         load_b(st + P::oB0, 0, kb);
-        if (w < 4)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(st + P::oSA + 4 * 64 * (w % P::kRS)), 4, savoff,
-                                                     (64 * (w % P::kRS) * A.s_pitch + kb) * 4, 0, 0);
-        else if constexpr (kRowB)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(st + P::oSB0 + 4 * sb_lrow), 4, sb_voff, kb * 4,
-                                                     0, 0);
+    };
+    // Quarter f % 4 of the scales of slices 4 (f / 4) .. + 3: every wave loads
+    // one run of 16 rows, four lanes a row (a load of one slice's scales would
+    // touch 64 rows, a line each).  Slice kb issues quarter kb + 6, so a group
+    // is whole three slices before it is read and its place has been free for two.
+    constexpr int kRuns = pp_scale_runs<kTM, kTN, kRowB>(), kGroup = 64 * kRuns;
+    auto load_scales = [&](int f, int place) {
+        const int run = min((f & 3) * 8 + w, kRuns - 1);
+        float *dst = sx + place * kGroup + 64 * run;
+        if (run < kTM / 16)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)dst, 4, sa_voff,
+                                                     (16 * run * A.s_pitch + (f & ~3)) * 4, 0, 0);
         else
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(st + P::oSB0 + 4 * 64 * (w - 4)), 4, sb_voff,
-                                                     kb * 4, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)dst, 4, sb_voff,
+                                                     (16 * (run - kTM / 16) * B.s_pitch + (f & ~3)) * 4, 0, 0);
     };
     auto load_g2 = [&](uint8_t *st, int kb) {
         load_b(st + P::oB1, 1, kb);
-        if constexpr (kRowB)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(st + P::oSB1 + 4 * sb_lrow), 4, sb_voff,
-                                                     (kQ * B.s_pitch + kb) * 4, 0, 0);
     };
 
     v4f acc[4][2 * kJT];
@@ -294,22 +300,24 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, const PPOper
                 for (int s = 0; s < 4; ++s) bw[jj][s] = widen8<FB>(b[jj][2 * s], b[jj][2 * s + 1]);
         }
     };
-    auto read_scales = [&](const uint8_t *st, int off_b, int h) {
-        const float *ssa = reinterpret_cast<const float *>(st + P::oSA);
-        const float *ssb = reinterpret_cast<const float *>(st + off_b);
+    // the scales of the slice whose group and slice start at sg (with the first
+    // half, A's and the 128x128 blocks'; B's rows per half)
+    auto read_scales = [&](const float *sg, int h) {
+        const float *sb = sg + 64 * (kTM / 16);
         if (h == 0) {
             // 128x128 blocks: a wave's columns lie in one column block
-            const float sb = kRowB ? 1.0f : ssb[kTN == 256 ? wn * P::kWC / 128 : 0];
+            const float blk = kRowB ? 1.0f : sb[kTN == 256 ? wn * P::kWC / 128 : 0];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float sa = ssa[wm * 64 + 16 * i + fr];
-                wi[i] = kRowB ? sa : sa * sb;
+                const float sa = sg[64 * (wm * 4 + i) + fr];
+                wi[i] = kRowB ? sa : sa * blk;
             }
         }
         if constexpr (kRowB) {
+            // half h's column tile jj is tile columns wn * kWC + kQ h + 16 jj ..
 #pragma unroll
             for (int jj = 0; jj < kJT; ++jj)
-                sbq[jj] = *reinterpret_cast<const v4f *>(ssb + wn * kQ + 16 * jj + 4 * fg);
+                sbq[jj] = *reinterpret_cast<const v4f *>(sb + 64 * ((wn * P::kWC + kQ * h) / 16 + jj) + 4 * fg);
         }
     };
     auto phase_end = [&](auto wc) {
@@ -324,11 +332,14 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, const PPOper
     using H0 = PhaseC<0>;
     using H1 = PhaseC<1>;
 
+    int place = 0, place6 = 1; // of slice kb's group of scales, and of slice kb + 6's
     auto slice = [&](int kb, uint8_t *cur, uint8_t *nxt) {
+        const float *sg = sx + place * kGroup + 16 * (kb & 3);
         read_a(cur);
         read_b(cur + P::oB0);
         tail(H1{});
-        read_scales(cur, P::oSB0, 0);
+        read_scales(sg, 0);
+        load_scales(kb + 6, place6);
         load_g2(nxt, kb + 1);
         widen_a();
         widen_b();
@@ -337,19 +348,23 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, const PPOper
         sync();
         read_b(cur + P::oB1);
         tail(H0{});
-        read_scales(cur, P::oSB1, 1);
+        read_scales(sg, 1);
         load_g1(cur, kb + 2);
         widen_b();
+        if ((kb & 3) == 3) place = place == kScaleGroups - 1 ? 0 : place + 1;
+        if (((kb + 6) & 3) == 3) place6 = place6 == kScaleGroups - 1 ? 0 : place6 + 1;
         sync_lds();
         compute(H1{});
         sync();
     };
 
     if (kblocks > 0) {
+#pragma unroll
+        for (int f = 0; f < 6; ++f) load_scales(f, f >> 2);
         load_g1(st0, 0);
         load_g2(st0, 0);
         load_g1(st1, 1);
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(G2 + G1, 15));
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(G2 - 1 + G1, 15));
     }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -428,6 +443,7 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t
     typedef PPShape<256, 256> P;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[P::kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t st1[P::kStage];
+    __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<256, 256, false>()];
     const int tiles_n = (N + 255) / 256, nk = K / kBK;
     GroupTiles<256> tiles(offsets, groups, rows);
     const int t = xcd_tile(blockIdx.x, tiles.total * tiles_n);
@@ -443,10 +459,10 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t
                       sB + ((int64_t)gt.group * (N / 128) + n0 / 128) * nk, b_blocks * nk * 4, nk};
     uint16_t *c = C + row0 * N + n0;
     if (a_rows > 128)
-        pp_tile<FA, FB, 256, 256, false, false, kBF16>(st0, st1, a, b, nk, b_blocks - 1, c, N, a_rows,
+        pp_tile<FA, FB, 256, 256, false, false, kBF16>(st0, st1, sx, a, b, nk, b_blocks - 1, c, N, a_rows,
                                                        b_rows);
     else
-        pp_tile<FA, FB, 128, 256, false, false, kBF16>(st0, st1, a, b, nk, b_blocks - 1, c, N, a_rows,
+        pp_tile<FA, FB, 128, 256, false, false, kBF16>(st0, st1, sx, a, b, nk, b_blocks - 1, c, N, a_rows,
                                                        b_rows);
 }
 
@@ -471,6 +487,18 @@ __device__ __forceinline__ void group_blocks(const int32_t *offsets, int groups,
     kbn = min(kbn, kbs - kb0);
 }
 
+// Tile i of an XCD's share of the groups' tiles (`per` each): every group's
+// tiles are split over the XCDs, so that they get equal shares of long and of
+// short contractions; an XCD's share of a group is a contiguous run of its
+// grouped order.  tile >= per: none.
+__device__ __forceinline__ void group_share(int xcd, int i, int per, int &e, int &tile)
+{
+    const int share = (per + kXcds - 1) / kXcds;
+    e = i / share;
+    const int j = i - e * share;
+    tile = xcd * share + j;
+}
+
 // wgrad in kTM x kTN tiles of one group's C per block.
 template <int FA, int FB, int kTM, int kTN, int DC>
 __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
@@ -481,12 +509,12 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     typedef PPShape<kTM, kTN> P;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[P::kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t st1[P::kStage];
+    __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<kTM, kTN, true>()];
     const int tiles_m = (M + kTM - 1) / kTM, tiles_n = (N + kTN - 1) / kTN, per = tiles_m * tiles_n;
-    const int t = xcd_tile(blockIdx.x, groups * per);
-    if (t >= groups * per) return;
-    const int e = t / per;
-    int tm, tn, kb0, kbn;
-    group_tile(t - e * per, tiles_m, tiles_n, tm, tn);
+    int e, tile, tm, tn, kb0, kbn;
+    group_share(blockIdx.x % kXcds, blockIdx.x / kXcds, per, e, tile);
+    if (e >= groups || tile >= per) return;
+    group_tile(tile, tiles_m, tiles_n, tm, tn);
     const int kbs = (int)(stride / 128);
     group_blocks(offsets, groups, rows, e, kbs, kb0, kbn);
     const int64_t m0 = (int64_t)tm * kTM, n0 = (int64_t)tn * kTN;
@@ -496,7 +524,7 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     const PPOperand b{B + n0 * stride + (int64_t)kb0 * 128, b_rows * pitch - kb0 * 128, pitch, sB + n0 * kbs + kb0,
                       (b_rows * kbs - kb0) * 4, kbs};
     uint8_t *c = reinterpret_cast<uint8_t *>(C) + (((int64_t)e * M + m0) * N + n0) * (DC == kF32 ? 4 : 2);
-    pp_tile<FA, FB, kTM, kTN, true, DC == kF32, DC>(st0, st1, a, b, kbn, 0, c, N, a_rows, b_rows);
+    pp_tile<FA, FB, kTM, kTN, true, DC == kF32, DC>(st0, st1, sx, a, b, kbn, 0, c, N, a_rows, b_rows);
 }
 
 template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
@@ -517,8 +545,8 @@ template <int FA, int FB> hipError_t launch_grouped_wgrad(const GroupedArgs &a)
 {
 #define FP8Q_WGRAD(TM, TN, DC)                                                                                       \
     grouped_wgrad_pp_kernel<FA, FB, TM, TN, DC>                                                                      \
-        <<<(unsigned)((int64_t)a.groups * ((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN) + kXcds), kBSThreads, 0,     \
-           a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N, a.stride, a.C)
+        <<<(unsigned)(a.groups * kXcds * ((((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN) + kXcds - 1) / kXcds)),     \
+           kBSThreads, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N, a.stride, a.C)
     if (a.c_dtype == kBF16) FP8Q_WGRAD(256, 256, kBF16);
     else FP8Q_WGRAD(256, 128, kF32);
 #undef FP8Q_WGRAD
