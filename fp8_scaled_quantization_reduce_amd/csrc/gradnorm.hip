@@ -57,14 +57,20 @@ template <> struct Vec8<__bf16> {
     static constexpr int kParts = 1;
 };
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, int64_t left, float (&v)[8])
+// The norm's pass reads with ordinary loads (tensors that fit the last-level
+// cache are then found there by the clipping pass); the clipping pass, which
+// touches everything for the last time, loads and stores (kLast) with the
+// non-temporal hint: 940 MB of fp32 523 -> 510 us, with four times the blocks
+// below 480 us.
+template <typename T, bool kLast> __device__ __forceinline__ void load8(const T *p, int64_t left, float (&v)[8])
 {
     typedef typename Vec8<T>::part P;
     constexpr int kE = 8 / Vec8<T>::kParts;
     if (left >= 8) {
 #pragma unroll
         for (int k = 0; k < Vec8<T>::kParts; ++k) {
-            const P w = reinterpret_cast<const P *>(p)[k];
+            const P *q = reinterpret_cast<const P *>(p) + k;
+            const P w = kLast ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
             for (int e = 0; e < kE; ++e) v[k * kE + e] = (float)w[e];
         }
@@ -84,7 +90,7 @@ template <typename T> __device__ __forceinline__ void store8(T *p, int64_t left,
             P w;
 #pragma unroll
             for (int e = 0; e < kE; ++e) w[e] = (T)v[k * kE + e];
-            reinterpret_cast<P *>(p)[k] = w;
+            __builtin_nontemporal_store(w, reinterpret_cast<P *>(p) + k);
         }
     } else {
 #pragma unroll
@@ -99,7 +105,7 @@ template <typename T> __device__ __forceinline__ double square_unit(const T *g, 
 #pragma unroll
     for (int u = 0; u < kUnitVecs; ++u) {
         const int64_t i = at + ((int64_t)u * kGnThreads + threadIdx.x) * 8;
-        load8<T>(g + i, n - i, v[u]);
+        load8<T, false>(g + i, n - i, v[u]);
     }
     double s = 0.0;
 #pragma unroll
@@ -160,7 +166,7 @@ __device__ __forceinline__ void scale_unit(const T *g, T *out, int64_t n, int64_
 #pragma unroll
     for (int u = 0; u < kUnitVecs; ++u) {
         const int64_t i = at + ((int64_t)u * kGnThreads + threadIdx.x) * 8;
-        load8<T>(g + i, n - i, v[u]);
+        load8<T, true>(g + i, n - i, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kUnitVecs; ++u) {
@@ -190,7 +196,9 @@ __global__ __launch_bounds__(kGnThreads) void clip_kernel(TensorTable t, const d
     }
 }
 
-constexpr int kSquareGrid = kParts, kClipGrid = 2048;
+// One partial per block bounds the first grid; the second is larger, so that
+// few blocks walk: 2048 blocks 510 us, 16384 480 us, 65536 497 us (940 MB).
+constexpr int kSquareGrid = kParts, kClipGrid = 16384;
 
 } // namespace
 

@@ -11,10 +11,10 @@
 // per lane, so a row piece is read and written in one contiguous run and a
 // block's maximum is a reduction over 16 lanes.
 // tile_both_kernel: 128 rows of a group x 128 columns per block of 256
-// lanes, four rows x 16 columns each.  Row blocks are 8 lanes, column blocks
-// the whole block (8 lanes of a wave, then four waves through LDS); the
-// column codes are transposed through LDS, so both copies leave as whole 128-
-// byte pieces.
+// lanes, four rows x 16 columns each, kept as loaded (widened where they
+// are used).  Row blocks are 8 lanes, column blocks the whole block (8 lanes of
+// a wave, then four waves through LDS); the column codes are transposed
+// through LDS, so both copies leave as whole 128-byte pieces.
 #include "fp8q_device.h"
 #include "fp8q_launch.h"
 #include "groups.h"
@@ -61,119 +61,204 @@ __device__ __forceinline__ int64_t source_row(const int32_t *index, int64_t x_ro
     return r >= 0 && r < x_rows ? r : -1;
 }
 
-template <int F, int DT>
+// Max over the 8 lanes of a row block (columns), and over the 8 lanes of a
+// wave that share columns, of two packed 16-bit or one 32-bit magnitude.
+template <int DT> __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b)
+{
+    if constexpr (DT == kF32) return max(a, b);
+    const u16x2 m = __builtin_elementwise_max(as_u16x2(a), as_u16x2(b));
+    return __builtin_bit_cast(uint32_t, m);
+}
+#define FP8Q_DPP(V, CTRL) (uint32_t) __builtin_amdgcn_update_dpp(0, (int)(V), CTRL, 0xF, 0xF, false)
+__device__ __forceinline__ uint32_t max_row_lanes(uint32_t m)
+{
+    m = max(m, FP8Q_DPP(m, 0xB1));  // lane ^ 1
+    m = max(m, FP8Q_DPP(m, 0x4E));  // lane ^ 2
+    return max(m, FP8Q_DPP(m, 0x141)); // mirror in 8: the other four
+}
+template <int DT> __device__ __forceinline__ uint32_t max_col_lanes(uint32_t m)
+{
+    m = mag_max<DT>(m, FP8Q_DPP(m, 0x128)); // rotate by 8 in 16: lane ^ 8
+    const auto p = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = mag_max<DT>((uint32_t)p[0], (uint32_t)p[1]);
+    const auto q = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return mag_max<DT>((uint32_t)q[0], (uint32_t)q[1]);
+}
+
+// kU rows at once: their index and data loads go out together.
+template <int F, int DT, int kU>
 __global__ __launch_bounds__(kGqThreads) void rows_kernel(const typename In<DT>::type *__restrict__ x, int64_t x_rows,
                                                           int64_t cols, const int32_t *__restrict__ index,
                                                           int64_t rows, uint8_t *__restrict__ q, float *__restrict__ s)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t pieces = (cols + 511) / 512, units = rows * pieces;
+    const int lane = threadIdx.x & 63, pieces = (int)((cols + 511) / 512);
+    const int64_t units = (rows + kU - 1) / kU * pieces;
     for (int64_t u = (int64_t)blockIdx.x * (kGqThreads / 64) + (threadIdx.x >> 6); u < units;
          u += (int64_t)gridDim.x * (kGqThreads / 64)) {
-        const int64_t t = u / pieces, c = (u - t * pieces) * 512 + 8 * lane;
-        const int64_t r = source_row(index, x_rows, t);
-        float v[8];
+        const int64_t t0 = u / pieces * kU;
+        const int c = (int)(u % pieces) * 512 + 8 * lane;
+        int64_t r[kU];
+        float v[kU][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+        for (int k = 0; k < kU; ++k) r[k] = t0 + k < rows ? source_row(index, x_rows, t0 + k) : -1;
         // cols is a multiple of 128, so the 16 lanes of a block agree
-        if (c < cols && r >= 0) load_n<DT, 8>(x + r * cols + c, v);
-        uint32_t m = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, f32_absbits(v[e]));
+        for (int k = 0; k < kU; ++k) {
+            if (c < cols && r[k] >= 0) {
+                load_n<DT, 8>(x + r[k] * cols + c, v[k]);
+            } else {
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-        const Scales sc = current_scales(__uint_as_float(canonical_amax_bits(m)), Fmt<F>::kMax, 0);
-        if (c < cols) {
-            uint2 o;
-            o.x = encode4<F>(v[0], v[1], v[2], v[3], sc.scale);
-            o.y = encode4<F>(v[4], v[5], v[6], v[7], sc.scale);
-            *reinterpret_cast<uint2 *>(q + t * cols + c) = o;
-            if ((lane & 15) == 0) s[t * (cols / 128) + c / 128] = sc.s;
+                for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kU; ++k) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max(m, f32_absbits(v[k][e]));
+            m = max_row_lanes(m);
+            m = max(m, FP8Q_DPP(m, 0x128)); // rotate by 8 in 16: the block's other eight lanes
+            const Scales sc = current_scales(__uint_as_float(canonical_amax_bits(m)), Fmt<F>::kMax, 0);
+            if (c < cols && t0 + k < rows) {
+                uint2 o;
+                if (__builtin_expect(m < kInfBits, 1)) { // finite block: no product is NaN
+                    o.x = encode4<F, false>(v[k][0], v[k][1], v[k][2], v[k][3], sc.scale);
+                    o.y = encode4<F, false>(v[k][4], v[k][5], v[k][6], v[k][7], sc.scale);
+                } else {
+                    o.x = encode4<F>(v[k][0], v[k][1], v[k][2], v[k][3], sc.scale);
+                    o.y = encode4<F>(v[k][4], v[k][5], v[k][6], v[k][7], sc.scale);
+                }
+                *reinterpret_cast<uint2 *>(q + (t0 + k) * cols + c) = o;
+                if ((lane & 15) == 0) s[(t0 + k) * (cols / 128) + c / 128] = sc.s;
+            }
         }
     }
 }
 
+// 16 elements of a row as loaded: 8 dwords of bf16 pairs or 16 of fp32.
+template <int DT> struct Piece {
+    static constexpr int kDw = DT == kF32 ? 16 : 8;
+    uint32_t d[kDw];
+    __device__ __forceinline__ void load(const typename In<DT>::type *p)
+    {
+#pragma unroll
+        for (int i = 0; i < kDw / 4; ++i) {
+            const uint4 w = reinterpret_cast<const uint4 *>(p)[i];
+            d[4 * i] = w.x, d[4 * i + 1] = w.y, d[4 * i + 2] = w.z, d[4 * i + 3] = w.w;
+        }
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < kDw; ++i) d[i] = 0u;
+    }
+    __device__ __forceinline__ float at(int e) const // e: compile-time
+    {
+        if constexpr (DT == kF32) return __uint_as_float(d[e]);
+        else return e & 1 ? bf16_hi(d[e >> 1]) : bf16_lo(d[e >> 1]);
+    }
+    // magnitudes of dword i
+    __device__ __forceinline__ uint32_t mag(int i) const
+    {
+        return d[i] & (DT == kF32 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
+    }
+};
+
 template <int F, int DT>
-__global__ __launch_bounds__(kGqThreads) void tile_both_kernel(
+__global__ __launch_bounds__(kGqThreads, 4) void tile_both_kernel(
     const typename In<DT>::type *__restrict__ x, int64_t x_rows, int64_t cols, const int32_t *__restrict__ index,
     int rows, const int32_t *__restrict__ offsets, int groups, uint8_t *__restrict__ q_row, float *__restrict__ s_row,
     uint8_t *__restrict__ q_col, float *__restrict__ s_col, int64_t stride)
 {
+    constexpr int kDw = Piece<DT>::kDw, kPer = 16 / kDw; // elements per dword
     __shared__ __attribute__((aligned(16))) uint32_t tl[128 * 32]; // column codes, [column][row / 4]
-    __shared__ uint32_t colmax[4][128];
+    __shared__ uint32_t colmax[4][128 / kPer];
     __shared__ float colscale[128];
+    __shared__ uint32_t colbad; // some column scale is NaN, infinite or zero
     const int blocks_c = (int)(cols / 128);
     const int t = (int)(blockIdx.x / blocks_c), cb = (int)(blockIdx.x % blocks_c);
     GroupTiles<128> tiles(offsets, groups, rows);
     if (t >= tiles.total) return;
     const GroupTile gt = tiles.find(t);
     const int ig = threadIdx.x >> 3, jg = threadIdx.x & 7, wave = threadIdx.x >> 6;
+    // the caller's columnwise buffers may be too short for these offsets
+    const bool fits = (int64_t)t * 128 + 128 <= stride; // block-uniform
+    const int first = 128 * gt.tile + 4 * ig, live = gt.size - first; // the lane's rows in the group
     const int64_t c0 = (int64_t)cb * 128 + 16 * jg;
-    float v[4][16];
+    Piece<DT> v[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const int in_group = 128 * gt.tile + 4 * ig + r;
-        const int64_t src = in_group < gt.size ? source_row(index, x_rows, (int64_t)gt.row0 + in_group) : -1;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[r][e] = 0.0f;
-        if (src >= 0) load_n<DT, 16>(x + src * cols + c0, v[r]);
+        const int64_t src = r < live ? source_row(index, x_rows, (int64_t)gt.row0 + first + r) : -1;
+        if (src >= 0) v[r].load(x + src * cols + c0);
+        else v[r].clear();
     }
     if (q_row) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m = max(m, f32_absbits(v[r][e]));
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+            for (int i = 0; i < kDw; ++i) m = mag_max<DT>(m, v[r].mag(i));
+            if constexpr (DT == kBF16) m = bf16_absmax_to_f32bits(as_u16x2(m));
+            m = max_row_lanes(m);
             const Scales sc = current_scales(__uint_as_float(canonical_amax_bits(m)), Fmt<F>::kMax, 0);
-            const int in_group = 128 * gt.tile + 4 * ig + r;
-            if (in_group < gt.size) {
-                const int64_t row = (int64_t)gt.row0 + in_group;
-                uint4 o;
-                o.x = encode4<F>(v[r][0], v[r][1], v[r][2], v[r][3], sc.scale);
-                o.y = encode4<F>(v[r][4], v[r][5], v[r][6], v[r][7], sc.scale);
-                o.z = encode4<F>(v[r][8], v[r][9], v[r][10], v[r][11], sc.scale);
-                o.w = encode4<F>(v[r][12], v[r][13], v[r][14], v[r][15], sc.scale);
-                *reinterpret_cast<uint4 *>(q_row + row * cols + c0) = o;
+            uint32_t o[4];
+            if (__builtin_expect(m < kInfBits, 1)) { // finite block: no product is NaN
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = encode4<F, false>(v[r].at(4 * k), v[r].at(4 * k + 1), v[r].at(4 * k + 2),
+                                             v[r].at(4 * k + 3), sc.scale);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = encode4<F>(v[r].at(4 * k), v[r].at(4 * k + 1), v[r].at(4 * k + 2), v[r].at(4 * k + 3),
+                                      sc.scale);
+            }
+            if (r < live) {
+                const int64_t row = (int64_t)gt.row0 + first + r;
+                *reinterpret_cast<uint4 *>(q_row + row * cols + c0) = make_uint4(o[0], o[1], o[2], o[3]);
                 if (jg == 0) s_row[row * blocks_c + cb] = sc.s;
             }
         }
     }
-    // the caller's columnwise buffers may be too short for these offsets
-    if ((int64_t)t * 128 + 128 > stride) return; // block-uniform
+    if (!fits) return;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m = max(m, f32_absbits(v[r][c]));
-#pragma unroll
-        for (int d = 8; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-        if ((threadIdx.x & 63) < 8) colmax[wave][16 * jg + c] = m;
+    for (int i = 0; i < kDw; ++i) {
+        uint32_t m = mag_max<DT>(mag_max<DT>(v[0].mag(i), v[1].mag(i)), mag_max<DT>(v[2].mag(i), v[3].mag(i)));
+        m = max_col_lanes<DT>(m);
+        if ((threadIdx.x & 63) < 8) colmax[wave][kDw * jg + i] = m;
     }
+    if (threadIdx.x == 0) colbad = 0;
     __syncthreads();
     if (threadIdx.x < 128) {
-        const int c = threadIdx.x;
-        const uint32_t m = max(max(colmax[0][c], colmax[1][c]), max(colmax[2][c], colmax[3][c]));
+        const int c = threadIdx.x, k = c / kPer;
+        uint32_t m = mag_max<DT>(mag_max<DT>(colmax[0][k], colmax[1][k]), mag_max<DT>(colmax[2][k], colmax[3][k]));
+        if constexpr (DT == kBF16) m = c & 1 ? m & 0xFFFF0000u : m << 16;
         const Scales sc = current_scales(__uint_as_float(canonical_amax_bits(m)), Fmt<F>::kMax, 0);
         colscale[c] = sc.scale;
+        if (m >= kInfBits) colbad = 1;
         s_col[((int64_t)cb * 128 + c) * (stride / 128) + t] = sc.s;
     }
     __syncthreads();
-    // four rows of a column are one dword; the 16-byte chunks of a column are
-    // XOR-ed with the column's lane, which spreads the writes over the banks
+    // four rows of a column are one dword; the 16-byte chunks of a
+    // column are XOR-ed with the column's lane, which spreads the
+    // writes over the banks
+    const bool bad = colbad != 0;
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
         const float sc = colscale[16 * jg + c];
-        tl[(16 * jg + c) * 32 + ((((ig >> 2) ^ jg) << 2) | (ig & 3))] =
-            encode4<F>(v[0][c], v[1][c], v[2][c], v[3][c], sc);
+        uint32_t o;
+        if (__builtin_expect(!bad, 1))
+            o = encode4<F, false>(v[0].at(c), v[1].at(c), v[2].at(c), v[3].at(c), sc);
+        else
+            o = encode4<F>(v[0].at(c), v[1].at(c), v[2].at(c), v[3].at(c), sc);
+        tl[(16 * jg + c) * 32 + ((((ig >> 2) ^ jg) << 2) | (ig & 3))] = o;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int c = 32 * k + (threadIdx.x >> 3), chunk = threadIdx.x & 7;
         const uint4 o = *reinterpret_cast<const uint4 *>(&tl[c * 32 + ((chunk ^ (c >> 4)) << 2)]);
-        *reinterpret_cast<uint4 *>(q_col + ((int64_t)cb * 128 + c) * stride + (int64_t)t * 128 + 16 * chunk) = o;
+        st_stream(q_col + ((int64_t)cb * 128 + c) * stride + (int64_t)t * 128 + 16 * chunk, o);
     }
 }
 
@@ -184,10 +269,15 @@ hipError_t launch(const void *x_, int64_t x_rows, int64_t cols, const int32_t *i
 {
     const typename In<DT>::type *x = (const typename In<DT>::type *)x_;
     if (!q_col) {
-        const int64_t units = rows * ((cols + 511) / 512), per = kGqThreads / 64;
+        const int64_t pieces = (cols + 511) / 512;
+        // four rows a wave in bf16 (16 bytes a lane and row) once that leaves
+        // enough waves to fill the chip: 16384x4096 44.0 -> 38.8 us; fp32, two
+        // loads a lane already, 5000x4096 is faster with one (19.1, 20.0 us)
+        const bool four = DT == kBF16 && rows * pieces >= 16384;
+        const int64_t units = (four ? (rows + 3) / 4 : rows) * pieces, per = kGqThreads / 64;
         const int64_t g = (units + per - 1) / per;
-        rows_kernel<F, DT><<<(int)(g < kMaxGrid ? g : kMaxGrid), kGqThreads, 0, s>>>(x, x_rows, cols, index, rows,
-                                                                                     q_row, s_row);
+        auto k = four ? rows_kernel<F, DT, 4> : rows_kernel<F, DT, 1>;
+        k<<<(int)(g < kMaxGrid ? g : kMaxGrid), kGqThreads, 0, s>>>(x, x_rows, cols, index, rows, q_row, s_row);
     } else {
         const int64_t g = max_tiles(rows, groups, 128) * (cols / 128);
         tile_both_kernel<F, DT><<<(unsigned)g, kGqThreads, 0, s>>>(x, x_rows, cols, index, (int)rows, offsets, groups,
