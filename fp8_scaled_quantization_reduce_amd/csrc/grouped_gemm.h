@@ -82,52 +82,78 @@ struct GroupedArgs {
     int cus;
 };
 
-// fprop / dgrad with 16 rows of a group x 64 columns per block; four waves
-// take the 128-wide slices in turn and add their sums through LDS.
-template <int FA, int FB, int DC>
-__global__ __launch_bounds__(256) void grouped_rows_kernel(const uint8_t *__restrict__ A, const float *__restrict__ sA,
-                                                           const uint8_t *__restrict__ B, const float *__restrict__ sB,
-                                                           const int32_t *__restrict__ offsets, int groups, int rows,
-                                                           int N, int K, void *__restrict__ C)
+// fprop / dgrad for few rows per group, where the weights' bytes are what
+// counts: 16 kMT rows of a group x 16 kNT columns per block, fragments loaded
+// straight from memory into registers (a weight byte is used by one wave).
+// kWK waves take the 128-wide slices in turn and add their sums through LDS.
+template <int FA, int FB, int kMT, int kNT, int kWK>
+__global__ __launch_bounds__(64 * kWK) void grouped_rows_kernel(const uint8_t *__restrict__ A,
+                                                                const float *__restrict__ sA,
+                                                                const uint8_t *__restrict__ B,
+                                                                const float *__restrict__ sB,
+                                                                const int32_t *__restrict__ offsets, int groups,
+                                                                int rows, int N, int K, uint16_t *__restrict__ C)
 {
-    __shared__ v4f sums[4][4][64];
-    const int tiles_n = N / 64;
-    const int t = blockIdx.x / tiles_n, n0 = (int)(blockIdx.x % tiles_n) * 64;
-    GroupTiles<16> tiles(offsets, groups, rows);
+    constexpr int kTM = 16 * kMT, kTN = 16 * kNT, kT = kMT * kNT;
+    __shared__ v4f sums[kWK][kT][64];
+    const int tiles_n = N / kTN;
+    const int t = blockIdx.x / tiles_n, n0 = (int)(blockIdx.x % tiles_n) * kTN;
+    GroupTiles<kTM> tiles(offsets, groups, rows);
     if (t >= tiles.total) return;
     const GroupTile gt = tiles.find(t);
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int nk = K / 128;
-    const int in_group = 16 * gt.tile + r;
-    const bool live = in_group < gt.size;
-    const int64_t row = gt.row0 + (live ? in_group : 16 * gt.tile);
-    const uint8_t *Bg = B + ((int64_t)gt.group * N + n0) * K;
+    const int left = gt.size - kTM * gt.tile; // rows of the tile in the group
+    const int64_t row0 = gt.row0 + kTM * gt.tile;
+    // rows past the group's last repeat it; their results are not stored
+    const uint8_t *Ar[kMT];
+    const float *sAr[kMT];
+#pragma unroll
+    for (int i = 0; i < kMT; ++i) {
+        const int64_t row = row0 + min(16 * i + r, left - 1);
+        Ar[i] = A + row * K;
+        sAr[i] = sA + row * nk;
+    }
+    const uint8_t *Bg = B + ((int64_t)gt.group * N + n0 + r) * K;
     const float *sBg = sB + ((int64_t)gt.group * (N / 128) + n0 / 128) * nk;
-    v4f acc[4];
+    v4f acc[kMT][kNT];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int kb = w; kb < nk; kb += 4) {
-        const v8i a = load_frag(A + row * K + kb * 128, g);
-        const float wt = sA[row * nk + kb] * sBg[kb];
+    for (int i = 0; i < kMT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const v8i b = load_frag(Bg + (int64_t)(16 * j + r) * K + kb * 128, g);
-            const v4f p = slice16<FA, FB, false>(b, a);
+        for (int j = 0; j < kNT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int kb = w; kb < nk; kb += kWK) {
+        v8i a[kMT], b[kNT];
+        float wt[kMT];
+        const float sb = sBg[kb];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = __builtin_fmaf(p[e], wt, acc[j][e]);
+        for (int j = 0; j < kNT; ++j) b[j] = load_frag(Bg + (int64_t)(16 * j) * K + kb * 128, g);
+#pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+            a[i] = load_frag(Ar[i] + kb * 128, g);
+            wt[i] = sAr[i][kb] * sb;
         }
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+                const v4f p = slice16<FA, FB, false>(b[j], a[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], wt[i], acc[i][j][e]);
+            }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sums[w][j][lane] = acc[j];
-    __syncthreads();
-    // wave w finishes column tile w
-    v4f c = sums[0][w][lane];
+    for (int i = 0; i < kMT; ++i)
 #pragma unroll
-    for (int k = 1; k < 4; ++k) c += sums[k][w][lane];
-    if (live) {
-        const int64_t at = row * N + n0 + 16 * w + 4 * g;
-        if constexpr (DC == kF32) *reinterpret_cast<v4f *>((float *)C + at) = c;
-        else *reinterpret_cast<uint2 *>((uint16_t *)C + at) = __builtin_bit_cast(uint2, __builtin_convertvector(c, bf16x4));
+        for (int j = 0; j < kNT; ++j) sums[w][i * kNT + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int q = w; q < kT; q += kWK) {
+        const int i = q / kNT, j = q % kNT;
+        v4f c = sums[0][q][lane];
+#pragma unroll
+        for (int k = 1; k < kWK; ++k) c += sums[k][q][lane];
+        if (16 * i + r < left)
+            *reinterpret_cast<uint2 *>(C + (row0 + 16 * i + r) * N + n0 + 16 * j + 4 * g) =
+                __builtin_bit_cast(uint2, __builtin_convertvector(c, bf16x4));
     }
 }
 
@@ -527,17 +553,60 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     pp_tile<FA, FB, kTM, kTN, true, DC == kF32, DC>(st0, st1, sx, a, b, kbn, 0, c, N, a_rows, b_rows);
 }
 
+// The tile of an fprop / dgrad launch.  Up to 12 rows a group on average most
+// groups fit a 16-row tile, so the weights are read once, and 32 columns a block are
+// faster than 16 unless the blocks then do not fill the chip (8 rows over
+// eight 14336 x 4096 matrices: 53.6 and 59.1 us; 64 columns 56.8 us).  Above,
+// a launch takes about `step` per round of one block per CU, `least` at the
+// least: both measured at K = 4096, one 4096-column matrix with 16 to 1024
+// rows, in us.  The steps grow slower than the tiles' areas, so the large
+// ping-pong tiles win as soon as they fill a part of the chip: 256 rows over
+// those eight matrices 109 us against 132 us in 32 x 64 tiles, but 40 rows of
+// one 4096 x 4096 matrix 11.7 us in 32 x 32 tiles against 29 us.
+enum RowsTile { kRows16x16, kRows16x32, kRows32x32, kRows32x64, kRows64x64, kRowsPP };
+
+inline RowsTile rows_tile(const GroupedArgs &a)
+{
+    const int64_t cus = a.cus > 0 ? a.cus : 256;
+    auto blocks = [&](int tm, int tn) { return max_tiles(a.rows, a.groups, tm) * ((a.N + tn - 1) / tn); };
+    const int64_t live = a.rows < a.groups ? a.rows : a.groups;
+    if (a.rows <= 12 * live) return blocks(16, 32) >= cus ? kRows16x32 : kRows16x16;
+    static const struct {
+        int tm, tn;
+        double least, step;
+    } cost[6] = {{16, 16, 8.7, 5.0},   {16, 32, 8.8, 7.2},   {32, 32, 11.5, 10.5},
+                 {32, 64, 15.4, 14.5}, {64, 64, 22.5, 22.0}, {256, 256, 40.0, 40.0}};
+    RowsTile best = kRowsPP;
+    double least = 0.0;
+    for (int i = kRowsPP; i >= kRows16x16; --i) {
+        const int64_t rounds = (blocks(cost[i].tm, cost[i].tn) + cus - 1) / cus;
+        double us = cost[i].step * (double)rounds;
+        if (i == kRowsPP && a.rows <= 128 * live) us *= 29.0 / 40.0; // mostly 128 x 256 tiles
+        if (us < cost[i].least) us = cost[i].least;
+        if (i == kRowsPP || us < least) best = (RowsTile)i, least = us;
+    }
+    return best;
+}
+
 template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
 {
-    if (a.rows > 16 * a.groups) {
+#define FP8Q_ROWS(MT, NT, WK)                                                                                        \
+    grouped_rows_kernel<FA, FB, MT, NT, WK>                                                                          \
+        <<<(unsigned)(max_tiles(a.rows, a.groups, 16 * MT) * (a.N / (16 * NT))), 64 * WK, 0, a.stream>>>(            \
+            a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C)
+    switch (rows_tile(a)) {
+    case kRows16x16: FP8Q_ROWS(1, 1, 8); break;
+    case kRows16x32: FP8Q_ROWS(1, 2, 8); break;
+    case kRows32x32: FP8Q_ROWS(2, 2, 8); break;
+    case kRows32x64: FP8Q_ROWS(2, 4, 4); break;
+    case kRows64x64: FP8Q_ROWS(4, 4, 4); break;
+    default: {
         const int64_t tiles = max_tiles(a.rows, a.groups, 256) * ((a.N + 255) / 256);
         grouped_pp_kernel<FA, FB><<<(unsigned)(tiles + kXcds), kBSThreads, 0, a.stream>>>(
             a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C);
-    } else {
-        const unsigned grid = (unsigned)(max_tiles(a.rows, a.groups, 16) * (a.N / 64));
-        grouped_rows_kernel<FA, FB, kBF16><<<grid, 256, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups,
-                                                                       a.rows, (int)a.N, (int)a.K, a.C);
     }
+    }
+#undef FP8Q_ROWS
     return hipGetLastError();
 }
 

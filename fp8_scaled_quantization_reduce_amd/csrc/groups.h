@@ -87,10 +87,11 @@ template <int kTile> struct GroupTiles {
     }
 };
 
-// The most tiles of `tile` rows that `groups` groups over `rows` rows can have.
+// The most tiles of `tile` rows that `groups` groups over `rows` rows can
+// have: sum ceil(m / tile) over at most min(groups, rows) groups with rows.
 inline int64_t max_tiles(int64_t rows, int groups, int tile)
 {
-    return rows / tile + (rows < groups ? rows : groups);
+    return (rows + (rows < groups ? rows : groups) * (tile - 1)) / tile;
 }
 
 } // namespace fp8q

@@ -210,6 +210,40 @@ def test_gemm_other_formats(fa, fb):
     check_gemm([30, 200], 256, 256, fa, fb)
 
 
+# one launch per tile that the rule on rows, groups and N picks (16 x 16 to
+# 64 x 64 blocks, the large tiles with full, half and one-row remainders), with
+# one, few, odd and even numbers of slices
+TILE_CASES = [([9, 0, 3], 128, 384), ([8] * 40, 256, 128), ([33, 7], 4096, 128), ([128], 4096, 256),
+              ([100, 141], 4096, 384), ([700, 130, 0, 1000, 170], 1152, 128), ([257, 1, 900, 384, 129], 1152, 384),
+              ([1100, 256, 512, 128], 1024, 640), ([2300], 896, 1152), ([1] * 30 + [1500, 0, 700], 1024, 256)]
+
+
+@pytest.mark.parametrize("k", range(len(TILE_CASES)))
+def test_gemm_tiles(k):
+    sizes, n, kk = TILE_CASES[k]
+    check_gemm(sizes, n, kk, E5 if k % 2 else E4, E4, seed=50 + k)
+
+
+def test_gemm_large_tiles_exact():
+    """Small integers and unit scales through the large tiles: every entry exact."""
+    rng = np.random.default_rng(18)
+    sizes, n, k = [700, 0, 131, 1290, 18, 256], 1152, 640
+    rows, groups = sum(sizes), len(sizes)
+    ai, bi = rng.integers(-2, 3, (rows, k)), rng.integers(-2, 3, (groups, n, k))
+    sa = 2.0 ** rng.integers(-1, 2, (rows, k // 128))
+    sb = 2.0 ** rng.integers(-1, 2, (groups, n // 128, k // 128))
+    c = torch.full((rows + 2, n), 777.0, dtype=torch.bfloat16, device="cuda")
+    fq.fp8_grouped_gemm(to_dev(oracle.encode(E4, ai.astype(np.float32))), E4, to_dev(sa.astype(np.float32)),
+                        to_dev(oracle.encode(E4, bi.astype(np.float32))), E4, to_dev(sb.astype(np.float32)),
+                        to_dev(offsets_of(sizes)), c[1:-1])
+    off = offsets_of(sizes)
+    for e in range(groups):
+        a = ai[off[e]:off[e + 1]] * np.repeat(sa[off[e]:off[e + 1]], 128, 1)
+        b = bi[e] * np.repeat(np.repeat(sb[e], 128, 0), 128, 1)
+        assert torch.equal(c[1 + off[e]:1 + off[e + 1]].cpu(), torch.from_numpy(a @ b.T).to(torch.bfloat16)), e
+    assert torch.all(c[0] == 777.0) and torch.all(c[-1] == 777.0)
+
+
 def test_gemm_rows_of_no_group():
     check_gemm([30, 0, 41], 128, 256, E4, E4, first=9, extra=13)
 
@@ -292,6 +326,29 @@ def test_wgrad_shapes(m, n, dtype):
 def test_wgrad_other_formats(fa, fb):
     for dtype in (torch.float32, torch.bfloat16):
         check_wgrad([130, 40], 128, 256, fa, fb, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wgrad_exact_integers(dtype):
+    """Small integers and unit scales over many slices: every entry exact."""
+    rng = np.random.default_rng(19)
+    sizes, m, n = [700, 0, 131, 1, 1290], 384, 640
+    pad = padded_of(sizes)
+    tp = int(pad[-1]) + 256
+    ai, bi = np.zeros((m, tp), int), np.zeros((n, tp), int)
+    for e, rows in enumerate(sizes):
+        ai[:, pad[e]:pad[e] + rows] = rng.integers(-2, 3, (m, rows))
+        bi[:, pad[e]:pad[e] + rows] = rng.integers(-2, 3, (n, rows))
+    sa, sb = 2.0 ** rng.integers(-1, 2, (m, tp // 128)), 2.0 ** rng.integers(-1, 2, (n, tp // 128))
+    c = torch.full((len(sizes), m, n), 777.0, dtype=dtype, device="cuda")
+    fq.fp8_grouped_gemm_wgrad(to_dev(oracle.encode(E5, ai.astype(np.float32))), E5, to_dev(sa.astype(np.float32)),
+                              to_dev(oracle.encode(E4, bi.astype(np.float32))), E4, to_dev(sb.astype(np.float32)),
+                              to_dev(offsets_of(sizes)), c)
+    for e in range(len(sizes)):
+        s = slice(int(pad[e]), int(pad[e + 1]))
+        sc = slice(int(pad[e]) // 128, int(pad[e + 1]) // 128)
+        want = (ai[:, s] * np.repeat(sa[:, sc], 128, 1)) @ (bi[:, s] * np.repeat(sb[:, sc], 128, 1)).T
+        assert torch.equal(c[e].cpu(), torch.from_numpy(want).to(dtype)), e
 
 
 def test_wgrad_every_code_is_widened_exactly():
