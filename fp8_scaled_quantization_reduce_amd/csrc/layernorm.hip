@@ -68,6 +68,26 @@ __device__ __forceinline__ void store_vec(typename Elem<DT>::type *p, bool has, 
     }
 }
 
+// kLast: read for the last time, so with the non-temporal hint (the backward
+// pass: 16384x4096 bf16 89.4 -> 87.4 us, 8192x4096 fp32 91.2 -> 86.5 us)
+template <int DT, bool kLast> __device__ __forceinline__ uint4 load_raw(const typename Elem<DT>::type *p, bool has)
+{
+    if (!has) return make_uint4(0u, 0u, 0u, 0u);
+    const typename Elem<DT>::raw *q = reinterpret_cast<const typename Elem<DT>::raw *>(p);
+    const typename Elem<DT>::raw r = kLast ? __builtin_nontemporal_load(q) : *q;
+    return make_uint4(r.x, r.y, r.z, r.w);
+}
+
+template <int DT, int kV> __device__ __forceinline__ void widen(const uint4 &w, float (&v)[kV])
+{
+    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (DT == kF32) v[k] = __uint_as_float(d[k]);
+        else v[2 * k] = bf16_lo(d[k]), v[2 * k + 1] = bf16_hi(d[k]);
+    }
+}
+
 // Sums over the R lanes that share a row (a wave, or the block through LDS:
 // one slot per wave and value, two sets used in turn so that one barrier per
 // reduction is enough).
@@ -104,39 +124,57 @@ template <int R, int kV, bool kFull> struct Cols {
     __device__ __forceinline__ int at_tail() const { return tail + t; }
 };
 
+// Each R-lane team walks its share of the rows: the next row is fetched before
+// the row in hand is reduced, and (kHeld) the gain and bias stay in registers.
 template <int DT, int PT, int R, int kI, bool kFull>
 __global__ __launch_bounds__(R > kLnThreads ? R : kLnThreads) void ln_fwd_kernel(
     const typename Elem<DT>::type *__restrict__ x, int64_t rows, int64_t cols_,
     const typename Elem<PT>::type *__restrict__ gamma, const typename Elem<PT>::type *__restrict__ beta, float eps,
     typename Elem<DT>::type *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd)
 {
+    typedef typename Elem<DT>::type T;
     constexpr int kV = Elem<DT>::kVec, kRows = R > kLnThreads ? 1 : kLnThreads / R;
-    constexpr bool kEarly = kI * kV <= 16; // gain and bias are fetched with the row
+    constexpr bool kHeld = kI * kV <= 16;
     __shared__ float lds[2][1][16];
     const Cols<R, kV, kFull> col(threadIdx.x % R, kFull ? R * kI * kV : (int)cols_);
     const float n = (float)col.cols;
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / R;
+    uint4 w[kI];
+    T wt = (T)0.0f;
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int i = 0; i < kI; ++i) w[i] = load_raw<DT, false>(x + r * col.cols + col.at(i), col.has(i));
+        if (col.has_tail()) wt = x[r * col.cols + col.at_tail()];
+    };
+    if (kHeld && row < rows) fetch(row);
+    float g[kHeld ? kI : 1][kV], b[kHeld ? kI : 1][kV], gt = 1.0f, bt = 0.0f;
+    if constexpr (kHeld) {
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+            if (gamma) load_vec<PT, kV>(gamma + col.at(i), col.has(i), g[i]);
+            if (beta) load_vec<PT, kV>(beta + col.at(i), col.has(i), b[i]);
+        }
+    }
+    if (col.has_tail()) {
+        if (gamma) gt = (float)gamma[col.at_tail()];
+        if (beta) bt = (float)beta[col.at_tail()];
+    }
     // a block whose rows are shared by all its lanes walks whole rounds, so
     // that every lane reaches the barriers
-    for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / R; row < rows; row += (int64_t)gridDim.x * kRows) {
-        const typename Elem<DT>::type *xr = x + row * col.cols;
-        typename Elem<DT>::type *yr = y + row * col.cols;
-        float v[kI][kV], g[kEarly ? kI : 1][kV], b[kEarly ? kI : 1][kV], vt = 0.0f;
+    for (; row < rows; row += step) {
+        T *yr = y + row * col.cols;
+        if constexpr (!kHeld) fetch(row);
+        float v[kI][kV], vt = (float)wt;
         float s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < kI; ++i) load_vec<DT, kV>(xr + col.at(i), col.has(i), v[i]);
-        if (col.has_tail()) vt = (float)xr[col.at_tail()];
-        if constexpr (kEarly) {
-#pragma unroll
-            for (int i = 0; i < kI; ++i) {
-                if (gamma) load_vec<PT, kV>(gamma + col.at(i), col.has(i), g[i]);
-                if (beta) load_vec<PT, kV>(beta + col.at(i), col.has(i), b[i]);
-            }
-        }
+        for (int i = 0; i < kI; ++i) widen<DT, kV>(w[i], v[i]);
+        if (kHeld && row + step < rows) fetch(row + step);
 #pragma unroll
         for (int i = 0; i < kI; ++i)
 #pragma unroll
             for (int e = 0; e < kV; ++e) s[0] += v[i][e];
-        s[0] += vt;
+        if (col.has_tail()) s[0] += vt;
         row_sum<R, 1>(s, lds, 0);
         const float mu = s[0] / n;
         float q[1] = {0.0f};
@@ -160,8 +198,8 @@ __global__ __launch_bounds__(R > kLnThreads ? R : kLnThreads) void ln_fwd_kernel
         }
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
-            constexpr int kP = kEarly ? 1 : 0;
-            if constexpr (!kEarly) {
+            constexpr int kP = kHeld ? 1 : 0;
+            if constexpr (!kHeld) {
                 if (gamma) load_vec<PT, kV>(gamma + col.at(i), col.has(i), g[0]);
                 if (beta) load_vec<PT, kV>(beta + col.at(i), col.has(i), b[0]);
             }
@@ -174,12 +212,7 @@ __global__ __launch_bounds__(R > kLnThreads ? R : kLnThreads) void ln_fwd_kernel
             }
             store_vec<DT, kV>(yr + col.at(i), col.has(i), v[i]);
         }
-        if (col.has_tail()) {
-            float o = vt * rs;
-            if (gamma) o *= (float)gamma[col.at_tail()];
-            if (beta) o += (float)beta[col.at_tail()];
-            yr[col.at_tail()] = (typename Elem<DT>::type)o;
-        }
+        if (col.has_tail()) yr[col.at_tail()] = (T)(vt * rs * gt + bt);
     }
 }
 
@@ -232,25 +265,6 @@ __global__ __launch_bounds__(kLnLong) void ln_fwd_long(const typename Elem<DT>::
 // The row's x and dy stay as loaded (bf16 pairs) and are widened again after
 // the reduction; the next row's are fetched before it, so that a team always
 // has a row in flight.
-template <int DT> __device__ __forceinline__ uint4 load_raw(const typename Elem<DT>::type *p, bool has)
-{
-    if (!has) return make_uint4(0u, 0u, 0u, 0u);
-    // read for the last time, so with the non-temporal hint (16384x4096 bf16
-    // 89.4 -> 87.4 us, 8192x4096 fp32 91.2 -> 86.5 us)
-    const typename Elem<DT>::raw r = __builtin_nontemporal_load(reinterpret_cast<const typename Elem<DT>::raw *>(p));
-    return make_uint4(r.x, r.y, r.z, r.w);
-}
-
-template <int DT, int kV> __device__ __forceinline__ void widen(const uint4 &w, float (&v)[kV])
-{
-    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (DT == kF32) v[k] = __uint_as_float(d[k]);
-        else v[2 * k] = bf16_lo(d[k]), v[2 * k + 1] = bf16_hi(d[k]);
-    }
-}
-
 template <int DT, int PT, int R, int kI, bool kFull>
 __global__ __launch_bounds__(R > kLnThreads ? R : kLnThreads, 2) void ln_bwd_kernel(
     const typename Elem<DT>::type *__restrict__ dy, const typename Elem<DT>::type *__restrict__ x, int64_t rows,
@@ -283,8 +297,8 @@ __global__ __launch_bounds__(R > kLnThreads ? R : kLnThreads, 2) void ln_bwd_ker
         r.mu = mean[row], r.rs = rstd[row];
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
-            r.x[i] = load_raw<DT>(x + row * col.cols + col.at(i), col.has(i));
-            r.dy[i] = load_raw<DT>(dy + row * col.cols + col.at(i), col.has(i));
+            r.x[i] = load_raw<DT, true>(x + row * col.cols + col.at(i), col.has(i));
+            r.dy[i] = load_raw<DT, true>(dy + row * col.cols + col.at(i), col.has(i));
         }
         if (col.has_tail()) r.xt = x[row * col.cols + col.at_tail()], r.dyt = dy[row * col.cols + col.at_tail()];
     };
@@ -522,6 +536,19 @@ int bwd_slots(int64_t rows, int64_t cols, int dtype)
     return bwd_blocks(rows, sh);
 }
 
+// Most blocks of the forward pass.  Where the gain and bias are held in
+// registers and the next row is fetched early, about what is resident at once
+// (16384x4096 bf16: 2048 blocks 51.6 us, one row a block 63.6; 30000x1111:
+// 40.4 and 45.0; 3000x16000 fp32: 512 blocks of 1024 lanes 72.7, 94.5); rows
+// that leave no registers for it take a block each (8192x8192 bf16 57.1 us,
+// 64.4 in 2048 blocks).
+int64_t fwd_blocks(LnShape sh, int vec)
+{
+    if (sh.lanes == 64) return 1024;
+    if (sh.lanes == 1024) return 512;
+    return sh.lanes && sh.vecs * vec <= 16 ? 2048 : kLnMaxGrid;
+}
+
 template <int DT, int PT>
 hipError_t fwd(const void *x_, int64_t rows, int64_t cols, const void *gamma_, const void *beta_, float eps, void *y_,
                float *mean, float *rstd, hipStream_t s)
@@ -534,7 +561,8 @@ hipError_t fwd(const void *x_, int64_t rows, int64_t cols, const void *gamma_, c
     const LnShape sh = fwd_shape(cols, Elem<DT>::kVec);
     const int per = sh.lanes == 64 ? kLnThreads / 64 : 1;
     int64_t g = (rows + per - 1) / per;
-    const int grid = (int)(g < kLnMaxGrid ? g : kLnMaxGrid);
+    const int64_t cap = fwd_blocks(sh, Elem<DT>::kVec), rounds = (g + cap - 1) / cap;
+    const int grid = (int)((g + rounds - 1) / rounds);
     const bool full = cols == (int64_t)sh.lanes * sh.vecs * Elem<DT>::kVec;
 #define FP8Q_LN(R, I)                                                                                                \
     if (sh.lanes == R && sh.vecs == I) {                                                                             \
