@@ -48,27 +48,6 @@ template <int F> __device__ __forceinline__ bf16x8 widen8(int lo, int hi)
     return bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
 }
 
-// One slice's 16x16 partial.  kWide: the codes are widened to bf16 and
-// multiplied by the bf16 matrix instruction, whose sums are binary32.
-// The FP8 instruction adds the products of eight neighbouring bytes on about
-// 15 bits under the largest of them (measured on the MI355X with one large
-// and one small product at a time), which leaves an fp32 result 1.1e-5 off in
-// the 2-norm where the widened one is 1e-8 off: below the rounding of a bf16
-// result, but above that of an fp32 one.
-template <int FA, int FB, bool kWide> __device__ __forceinline__ v4f slice16(const v8i &b, const v8i &a)
-{
-    if constexpr (!kWide) {
-        return mfma16x16x128<FB, FA>(b, a, v4f{0.f, 0.f, 0.f, 0.f});
-    } else {
-        v4f c{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8<FB>(b[2 * s], b[2 * s + 1]),
-                                                        widen8<FA>(a[2 * s], a[2 * s + 1]), c, 0, 0, 0);
-        return c;
-    }
-}
-
 struct GroupedArgs {
     const uint8_t *A, *B;
     const float *sA, *sB;
@@ -136,7 +115,7 @@ __global__ __launch_bounds__(64 * kWK) void grouped_rows_kernel(const uint8_t *_
         for (int i = 0; i < kMT; ++i)
 #pragma unroll
             for (int j = 0; j < kNT; ++j) {
-                const v4f p = slice16<FA, FB, false>(b[j], a[i]);
+                const v4f p = mfma16x16x128<FB, FA>(b[j], a[i], v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], wt[i], acc[i][j][e]);
             }
@@ -158,19 +137,14 @@ __global__ __launch_bounds__(64 * kWK) void grouped_rows_kernel(const uint8_t *_
 }
 
 // ---------------------------------------------------------------------------
-// One kTM x kTN tile of C on eight waves, the ping-pong schedule of
+// One kTM x 256 tile of C (bf16) on eight waves, the ping-pong schedule of
 // gemm_bs_pp_kernel for ragged operands: A and B rows past the tile's own are
 // loaded as zeros (the buffer records end there) and never stored, and the
 // contraction may start anywhere in the operands' rows (wgrad).
 //
 // Waves: kTM / 64 row strips x kTN / kWC column strips of 64 x kWC, group X
 // (waves 0-3) the left half of the columns, Y the right half.  256 x 256 tiles
-// have 64 x 128 waves; 128 x 256 and 256 x 128 tiles, for the rows a group
-// leaves over and for the widened products, 64 x 64.
-//
-// kWide (fp32 results): a read phase also widens the fragments it has read to
-// bf16, while the other group's matrix instructions run, and a compute phase
-// chains four bf16 instructions per 16x16 tile and slice.
+// have 64 x 128 waves; 128 x 256 tiles, for the rows a group leaves over, 64 x 64.
 struct PPOperand {
     const uint8_t *base; // first row of the tile, first byte of the contraction
     int bytes;           // readable from base
@@ -179,7 +153,8 @@ struct PPOperand {
     int s_bytes, s_pitch; // readable bytes; floats of a row (of blocks)
 };
 
-template <int kTM, int kTN> struct PPShape {
+template <int kTM> struct PPShape {
+    static constexpr int kTN = 256;
     static constexpr int kRS = kTM / 64;            // row strips
     static constexpr int kCS = 8 / kRS;             // column strips
     static constexpr int kWC = kTN / kCS;           // a wave's columns
@@ -191,13 +166,14 @@ template <int kTM, int kTN> struct PPShape {
 // Scales of four slices, three groups of them in LDS: a run of 16 rows is 64
 // floats, [slice][row].
 constexpr int kScaleGroups = 3;
-template <int kTM, int kTN, bool kRowB> constexpr int pp_scale_runs() { return kTM / 16 + (kRowB ? kTN / 16 : 1); }
+template <int kTM, bool kRowB> constexpr int pp_scale_runs() { return kTM / 16 + (kRowB ? 16 : 1); }
 
-template <int FA, int FB, int kTM, int kTN, bool kRowB, bool kWide, int DC>
-__device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, const PPOperand &A, const PPOperand &B, int kblocks,
-                                        int sb_last, void *C, int64_t ldc, int c_rows, int c_cols)
+template <int FA, int FB, int kTM, bool kRowB>
+__device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, const PPOperand &A, const PPOperand &B,
+                                        int kblocks, int sb_last, uint16_t *C, int64_t ldc, int c_rows, int c_cols)
 {
-    typedef PPShape<kTM, kTN> P;
+    constexpr int kTN = 256;
+    typedef PPShape<kTM> P;
     constexpr int kQ = P::kQ, kJT = P::kJT;
     constexpr int kAL = kTM / 64, kBL = kTN / 128; // loads per wave of A, of a B half
     constexpr int G1 = kAL + kBL, G2 = kBL + 1; // G2 with the slice's load of scales
@@ -240,7 +216,7 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
     // one run of 16 rows, four lanes a row (a load of one slice's scales would
     // touch 64 rows, a line each).  Slice kb issues quarter kb + 6, so a group
     // is whole three slices before it is read and its place has been free for two.
-    constexpr int kRuns = pp_scale_runs<kTM, kTN, kRowB>(), kGroup = 64 * kRuns;
+    constexpr int kRuns = pp_scale_runs<kTM, kRowB>(), kGroup = 64 * kRuns;
     auto load_scales = [&](int f, int place) {
         const int run = min((f & 3) * 8 + w, kRuns - 1);
         float *dst = sx + place * kGroup + 64 * run;
@@ -261,7 +237,6 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
 #pragma unroll
         for (int j = 0; j < 2 * kJT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     v8i a[4], b[kJT];                         // the slice's A fragments, the half's B fragments
-    bf16x8 aw[kWide ? 4 : 1][4], bw[kWide ? kJT : 1][4]; // the same widened
     float wi[4];
     v4f sbq[kJT];
     v4f pr[3]; // results awaiting promotion (tile t in pr[t % 3])
@@ -279,23 +254,13 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
     auto compute = [&](auto hc) {
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
-            if constexpr (kWide) {
-                v4f c{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[t >> 2][s], aw[t & 3][s], c, 0, 0, 0);
-                pr[t % 3] = c;
-            } else {
-                pr[t % 3] = mfma16x16x128<FB, FA>(b[t >> 2], a[t & 3], v4f{0.f, 0.f, 0.f, 0.f});
-            }
+            pr[t % 3] = mfma16x16x128<FB, FA>(b[t >> 2], a[t & 3], v4f{0.f, 0.f, 0.f, 0.f});
             if (t >= 2) promote(hc, t - 2);
         }
-        if constexpr (!kWide) {
 #pragma unroll
-            for (int t = 0; t < kT; ++t) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // MFMA
-                if (t >= 2) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); // promotion FMAs
-            }
+        for (int t = 0; t < kT; ++t) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // MFMA
+            if (t >= 2) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); // promotion FMAs
         }
     };
     auto tail = [&](auto hc) {
@@ -310,29 +275,13 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
 #pragma unroll
         for (int jj = 0; jj < kJT; ++jj) b[jj] = read_frag(st, wn * kQ + 16 * jj + fr, fg);
     };
-    auto widen_a = [&]() {
-        if constexpr (kWide) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) aw[i][s] = widen8<FA>(a[i][2 * s], a[i][2 * s + 1]);
-        }
-    };
-    auto widen_b = [&]() {
-        if constexpr (kWide) {
-#pragma unroll
-            for (int jj = 0; jj < kJT; ++jj)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) bw[jj][s] = widen8<FB>(b[jj][2 * s], b[jj][2 * s + 1]);
-        }
-    };
     // the scales of the slice whose group and slice start at sg (with the first
     // half, A's and the 128x128 blocks'; B's rows per half)
     auto read_scales = [&](const float *sg, int h) {
         const float *sb = sg + 64 * (kTM / 16);
         if (h == 0) {
             // 128x128 blocks: a wave's columns lie in one column block
-            const float blk = kRowB ? 1.0f : sb[kTN == 256 ? wn * P::kWC / 128 : 0];
+            const float blk = kRowB ? 1.0f : sb[wn * P::kWC / 128];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float sa = sg[64 * (wm * 4 + i) + fr];
@@ -367,8 +316,6 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
         read_scales(sg, 0);
         load_scales(kb + 6, place6);
         load_g2(nxt, kb + 1);
-        widen_a();
-        widen_b();
         sync_lds();
         compute(H0{});
         sync();
@@ -376,7 +323,6 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
         tail(H0{});
         read_scales(sg, 1);
         load_g1(cur, kb + 2);
-        widen_b();
         if ((kb & 3) == 3) place = place == kScaleGroups - 1 ? 0 : place + 1;
         if (((kb + 6) & 3) == 3) place6 = place6 == kScaleGroups - 1 ? 0 : place6 + 1;
         sync_lds();
@@ -415,8 +361,7 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
     asm volatile("" ::: "memory");
 
     // epilogue: each wave stages its 64 x kWC results and stores whole row pieces
-    constexpr int kB = DC == kF32 ? 4 : 2;
-    typedef EpiStage<P::kWC, kB, 64, P::kWC * kBK> ES;
+    typedef EpiStage<P::kWC, 2, 64, P::kWC * kBK> ES;
     const int wrow = wm * 64, wcol = wn * P::kWC;
     const bool inside = wrow < c_rows && wcol < c_cols;
     uint8_t *ep = (w < 4 ? st0 : st1) + (w & 3) * (P::kWC * kBK);
@@ -432,7 +377,7 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
 #pragma unroll
                 for (int j = 0; j < 2 * kJT; ++j)
                     ES::put(ep, 16 * i + fr - ps * ES::kPassRows, 4 * j + fg,
-                            pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, acc[i][j], m, none, 0.0f));
+                            pack_out4<kOutBF16, false, false>(0, acc[i][j], m, none, 0.0f));
             }
         }
         __syncthreads();
@@ -443,7 +388,7 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
             for (int s = 0; s < ES::kPassRows / ES::kRowsPerStore; ++s) {
                 const int r = s * ES::kRowsPerStore + rr, row = wrow + ps * ES::kPassRows + r;
                 const uint4 v = *reinterpret_cast<const uint4 *>(ep + ES::addr(r, c));
-                if (row < c_rows) st_stream(Cb + ((int64_t)row * ldc + wcol) * kB + 16 * c, v);
+                if (row < c_rows) st_stream(Cb + ((int64_t)row * ldc + wcol) * 2 + 16 * c, v);
             }
         }
     }
@@ -466,10 +411,10 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t
                                                                    const int32_t *__restrict__ offsets, int groups,
                                                                    int rows, int N, int K, uint16_t *__restrict__ C)
 {
-    typedef PPShape<256, 256> P;
+    typedef PPShape<256> P;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[P::kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t st1[P::kStage];
-    __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<256, 256, false>()];
+    __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<256, false>()];
     const int tiles_n = (N + 255) / 256, nk = K / kBK;
     GroupTiles<256> tiles(offsets, groups, rows);
     const int t = xcd_tile(blockIdx.x, tiles.total * tiles_n);
@@ -485,11 +430,9 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t
                       sB + ((int64_t)gt.group * (N / 128) + n0 / 128) * nk, b_blocks * nk * 4, nk};
     uint16_t *c = C + row0 * N + n0;
     if (a_rows > 128)
-        pp_tile<FA, FB, 256, 256, false, false, kBF16>(st0, st1, sx, a, b, nk, b_blocks - 1, c, N, a_rows,
-                                                       b_rows);
+        pp_tile<FA, FB, 256, false>(st0, st1, sx, a, b, nk, b_blocks - 1, c, N, a_rows, b_rows);
     else
-        pp_tile<FA, FB, 128, 256, false, false, kBF16>(st0, st1, sx, a, b, nk, b_blocks - 1, c, N, a_rows,
-                                                       b_rows);
+        pp_tile<FA, FB, 128, false>(st0, st1, sx, a, b, nk, b_blocks - 1, c, N, a_rows, b_rows);
 }
 
 // Blocks of 128 tokens before group e and in it (wave-uniform).
@@ -525,17 +468,18 @@ __device__ __forceinline__ void group_share(int xcd, int i, int per, int &e, int
     tile = xcd * share + j;
 }
 
-// wgrad in kTM x kTN tiles of one group's C per block.
-template <int FA, int FB, int kTM, int kTN, int DC>
+// wgrad with bf16 results in 256 x 256 tiles of one group's C.
+template <int FA, int FB>
 __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,
     const float *__restrict__ sB, const int32_t *__restrict__ offsets, int groups, int rows, int M, int N,
-    int64_t stride, void *__restrict__ C)
+    int64_t stride, uint16_t *__restrict__ C)
 {
-    typedef PPShape<kTM, kTN> P;
+    constexpr int kTM = 256, kTN = 256;
+    typedef PPShape<kTM> P;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[P::kStage];
     __shared__ __attribute__((aligned(1024))) uint8_t st1[P::kStage];
-    __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<kTM, kTN, true>()];
+    __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<kTM, true>()];
     const int tiles_m = (M + kTM - 1) / kTM, tiles_n = (N + kTN - 1) / kTN, per = tiles_m * tiles_n;
     int e, tile, tm, tn, kb0, kbn;
     group_share(blockIdx.x % kXcds, blockIdx.x / kXcds, per, e, tile);
@@ -549,8 +493,198 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
                       (a_rows * kbs - kb0) * 4, kbs};
     const PPOperand b{B + n0 * stride + (int64_t)kb0 * 128, b_rows * pitch - kb0 * 128, pitch, sB + n0 * kbs + kb0,
                       (b_rows * kbs - kb0) * 4, kbs};
-    uint8_t *c = reinterpret_cast<uint8_t *>(C) + (((int64_t)e * M + m0) * N + n0) * (DC == kF32 ? 4 : 2);
-    pp_tile<FA, FB, kTM, kTN, true, DC == kF32, DC>(st0, st1, sx, a, b, kbn, 0, c, N, a_rows, b_rows);
+    uint16_t *c = C + ((int64_t)e * M + m0) * N + n0;
+    pp_tile<FA, FB, kTM, true>(st0, st1, sx, a, b, kbn, 0, c, N, a_rows, b_rows);
+}
+
+// wgrad in 128 x 128 tiles, four waves of 64 x 64 per block, two blocks per
+// CU: one block's stores and first loads run beside the other's products.  A
+// wave reads its share of a slice from LDS into registers at once, so the
+// stage is free for the slice after next while the products run.
+//
+// fp32 results: the codes are widened to bf16 (exact) and multiplied by the
+// bf16 matrix instruction, whose sums are binary32.  The FP8 instruction adds
+// the products of eight neighbouring bytes on about 15 bits under the largest
+// of them (measured on the MI355X with one large and one small product at a
+// time), which leaves an fp32 result 1.1e-5 off in the 2-norm where the widened
+// one is 7e-8 off: below the rounding of a bf16 result, above that of an fp32 one.
+//
+// Eight 14336 x 4096 gradients over 8192 tokens, fp32: 1.20 ms, 0.80 PFLOP/s,
+// 1.9 GB written.  The chip's power bounds it: in 256 x 128 ping-pong tiles of
+// one block per CU the same work took 30% more cycles at a 25% higher clock
+// (2.91 million at 2.25 GHz, here 2.23 at 1.78).  Without the loads of the
+// slices it would take 15% less time, without the widening 11%, without the
+// scales 9%.  With 1024 tokens, where the stores count, 118 us against 146.
+template <int FA, int FB, int DC>
+__global__ __launch_bounds__(256, 2) void grouped_wgrad_kernel(
+    const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,
+    const float *__restrict__ sB, const int32_t *__restrict__ offsets, int groups, int rows, int M, int N,
+    int64_t stride, void *__restrict__ C)
+{
+    constexpr bool kWide = DC == kF32;
+    constexpr int kTile = 128, kOp = kTile * kBK, kSx = 16 * 64;
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * kOp];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1[2 * kOp];
+    __shared__ __attribute__((aligned(16))) float sx0[kSx];
+    __shared__ __attribute__((aligned(16))) float sx1[kSx];
+    const int tiles_m = M / kTile, tiles_n = N / kTile, per = tiles_m * tiles_n;
+    int e, tile, tm, tn, kb0, kbn;
+    group_share(blockIdx.x % kXcds, blockIdx.x / kXcds, per, e, tile);
+    if (e >= groups || tile >= per) return;
+    group_tile(tile, tiles_m, tiles_n, tm, tn);
+    const int kbs = (int)(stride / 128), pitch = (int)stride;
+    group_blocks(offsets, groups, rows, e, kbs, kb0, kbn);
+    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = w & 1, wn = w >> 1, fr = lane & 31, fg = lane >> 5;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(A + m0 * stride + (int64_t)kb0 * 128), 0, kTile * pitch - kb0 * 128, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(B + n0 * stride + (int64_t)kb0 * 128), 0, kTile * pitch - kb0 * 128, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc((void *)(sA + m0 * kbs + kb0), 0,
+                                                                         (kTile * kbs - kb0) * 4, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc((void *)(sB + n0 * kbs + kb0), 0,
+                                                                         (kTile * kbs - kb0) * 4, kRawBufferWord3);
+    const int voff = (lane >> 3) * pitch + (((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) << 4);
+    const int svoff = ((lane & 15) * kbs + (lane >> 4)) * 4;
+
+    // past the last slice the offset lies outside the buffer: nothing is read
+    auto load = [&](uint8_t *st, int kb) {
+        const int at = kb < kbn ? kb * kBK : 1 << 30;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int row = 8 * (w + 4 * u);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(st + row * kBK), 16, voff, row * pitch + at, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(st + kOp + row * kBK), 16, voff, row * pitch + at,
+                                                     0, 0);
+        }
+    };
+    auto load_scales = [&](float *sx, int kb) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int run = w + 4 * u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(sx + 64 * run), 4, svoff,
+                                                     (16 * run * kbs + kb) * 4, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(sx + 64 * (8 + run)), 4, svoff,
+                                                     (16 * run * kbs + kb) * 4, 0, 0);
+        }
+    };
+    v16f acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    // 32 rows x 128 K bytes: lane (fr, fg) takes chunks 4 fg .. 4 fg + 3 of row fr
+    auto read = [&](const uint8_t *st, int row, uint4(&o)[4]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = *reinterpret_cast<const uint4 *>(st + swz(row + fr, 4 * fg + c));
+    };
+    // step s of 16 K, widened
+    auto step = [&](auto fmt, const uint4(&v)[4], int s) {
+        const uint4 c = v[s >> 1];
+        return s & 1 ? widen8<decltype(fmt)::value>((int)c.z, (int)c.w)
+                     : widen8<decltype(fmt)::value>((int)c.x, (int)c.y);
+    };
+    auto half = [&](const uint4(&v)[4], int s) {
+        const uint4 lo = v[2 * s], hi = v[2 * s + 1];
+        return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+    // one slice: all codes are read first, so that `then` can refill the stage
+    auto slice = [&](uint8_t *st, const float *sg, auto then) {
+        uint4 a[2][4], b[2][4];
+        float wi[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) read(st, wm * 64 + 32 * i, a[i]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) read(st + kOp, wn * 64 + 32 * j, b[j]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wi[i] = sg[64 * (wm * 4 + 2 * i + (fr >> 4)) + (fr & 15)];
+        bf16x8 aw[kWide ? 2 : 1][8];
+        if constexpr (kWide) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int s = 0; s < 8; ++s) aw[i][s] = step(PhaseC<FA>{}, a[i], s);
+        }
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        then();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            v16f p[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) p[i][r] = 0.0f;
+            if constexpr (kWide) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const bf16x8 bw = step(PhaseC<FB>{}, b[j], s);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        p[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw, aw[i][s], p[i], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        p[i] = mfma32x32x64<FB, FA>(half(b[j], s), half(a[i], s), p[i]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v4f sb = *reinterpret_cast<const v4f *>(sg + 64 * (8 + wn * 4 + 2 * j + (q >> 1)) +
+                                                              8 * (q & 1) + 4 * fg);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j][4 * q + r] = __builtin_fmaf(p[i][4 * q + r], wi[i] * sb[r], acc[i][j][4 * q + r]);
+            }
+        }
+    };
+    load_scales(sx0, 0);
+    load(st0, 0);
+    load(st1, 1);
+    for (int kb = 0;; kb += 8) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (kb + u >= kbn) goto done;
+            // this slice's loads have landed; the next one's (and the scales) may be in flight
+            if ((u & 3) == 1) __builtin_amdgcn_s_waitcnt(waitcnt_imm(12, 15));
+            else __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 15));
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            slice(u & 1 ? st1 : st0, (u & 4 ? sx1 : sx0) + 16 * (u & 3), [&]() {
+                if ((u & 3) == 0) load_scales(u & 4 ? sx0 : sx1, kb + u + 4);
+                load(u & 1 ? st1 : st0, kb + u + 2);
+            });
+        }
+    }
+done:
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __syncthreads();
+    // each wave stages its 64 x 64 results and stores whole row pieces
+    typedef EpiStage<64, DC == kF32 ? 4 : 2, 64, 16384> ES;
+    uint32_t m = 0;
+    const Epi none{nullptr, kActNone, nullptr};
+    uint8_t *ep = (w < 2 ? st0 : st1) + (w & 1) * 16384;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v4f v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                ES::put(ep, 32 * i + fr, 8 * j + 2 * q + fg,
+                        pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, v, m, none, 0.0f));
+            }
+    __syncthreads();
+    ES::store(ep, C, N, (int64_t)e * M + m0 + wm * 64, n0 + wn * 64, lane);
 }
 
 // The tile of an fprop / dgrad launch.  Up to 12 rows a group on average most
@@ -610,15 +744,36 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
     return hipGetLastError();
 }
 
+// The tile of a bf16 wgrad launch, from the time of a round of one 256 x 256
+// tile or two 128 x 128 tiles per CU, in us, s slices of 128 tokens per group on
+// average (eight 4096 x 4096 gradients, 1 to 32 slices: 83 to 570 us in the
+// large tiles, 82 to 730 us in the small ones).  The large tiles reuse what they
+// read more, the small ones fill the chip where there are few: one 1408 x 2048
+// gradient over 32768 tokens 211 us, in large tiles 370 us.
+inline bool wgrad_large_tiles(const GroupedArgs &a)
+{
+    const int64_t cus = a.cus > 0 ? a.cus : 256;
+    auto rounds = [&](int tile, int64_t wide) {
+        return (double)((a.groups * ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile) + wide - 1) / wide);
+    };
+    const double s = (double)a.rows / 128.0 / a.groups;
+    return rounds(256, cus) * (8.5 + 1.9 * s) <= rounds(128, 2 * cus) * (3.9 + 1.3 * s);
+}
+
 template <int FA, int FB> hipError_t launch_grouped_wgrad(const GroupedArgs &a)
 {
-#define FP8Q_WGRAD(TM, TN, DC)                                                                                       \
-    grouped_wgrad_pp_kernel<FA, FB, TM, TN, DC>                                                                      \
-        <<<(unsigned)(a.groups * kXcds * ((((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN) + kXcds - 1) / kXcds)),     \
-           kBSThreads, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N, a.stride, a.C)
-    if (a.c_dtype == kBF16) FP8Q_WGRAD(256, 256, kBF16);
-    else FP8Q_WGRAD(256, 128, kF32);
-#undef FP8Q_WGRAD
+    auto grid = [&](int tile) {
+        const int64_t per = ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile);
+        return (unsigned)(a.groups * (int64_t)kXcds * ((per + kXcds - 1) / kXcds));
+    };
+    if (a.c_dtype == kBF16 && wgrad_large_tiles(a)) {
+        grouped_wgrad_pp_kernel<FA, FB><<<grid(256), kBSThreads, 0, a.stream>>>(
+            a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N, a.stride, (uint16_t *)a.C);
+    } else {
+        auto k = a.c_dtype == kBF16 ? grouped_wgrad_kernel<FA, FB, kBF16> : grouped_wgrad_kernel<FA, FB, kF32>;
+        k<<<grid(128), 256, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N,
+                                           a.stride, a.C);
+    }
     return hipGetLastError();
 }
 
