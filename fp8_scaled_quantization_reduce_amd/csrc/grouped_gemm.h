@@ -394,22 +394,17 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
     }
 }
 
-// Block b of a grid -> tile of `n` tiles, each XCD a contiguous run; >= n: none.
-__device__ __forceinline__ int xcd_tile(int b, int n)
-{
-    const int per = (n + kXcds - 1) / kXcds, i = b / kXcds;
-    return i < per ? (b % kXcds) * per + i : n;
-}
-
 // fprop / dgrad in tiles of 256 rows x 256 columns; a group's last tile of at
-// most 128 rows runs as a 128 x 256 tile.
+// most 128 rows runs as a 128 x 256 tile.  Each XCD has a contiguous run of
+// the tiles; what it leaves for a last round on at most half of its CUs runs as
+// two 128 x 256 tiles each.
 template <int FA, int FB>
 __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t *__restrict__ A,
                                                                    const float *__restrict__ sA,
                                                                    const uint8_t *__restrict__ B,
                                                                    const float *__restrict__ sB,
                                                                    const int32_t *__restrict__ offsets, int groups,
-                                                                   int rows, int N, int K, uint16_t *__restrict__ C)
+                                                                   int rows, int N, int K, uint16_t *__restrict__ C, int cus)
 {
     typedef PPShape<256> P;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[P::kStage];
@@ -417,13 +412,23 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t
     __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<256, false>()];
     const int tiles_n = (N + 255) / 256, nk = K / kBK;
     GroupTiles<256> tiles(offsets, groups, rows);
-    const int t = xcd_tile(blockIdx.x, tiles.total * tiles_n);
-    if (t >= tiles.total * tiles_n) return;
+    const int n = tiles.total * tiles_n, per = (n + kXcds - 1) / kXcds, first = (int)(blockIdx.x % kXcds) * per;
+    const int share = min(per, n - first); // this XCD's tiles
+    int i = blockIdx.x / kXcds, half = -1;
+    const int last = share % cus;
+    if (i >= share - last && 2 * last <= cus) {
+        half = (i - (share - last)) & 1;
+        i = share - last + ((i - (share - last)) >> 1);
+    }
+    if (i >= share) return;
+    const int t = first + i;
     const GroupTile gt = tiles.find(t / tiles_n);
     int tm, tn;
     group_tile(gt.tile * tiles_n + t % tiles_n, (gt.size + 255) / 256, tiles_n, tm, tn);
-    const int64_t row0 = gt.row0 + 256 * tm, n0 = 256 * tn;
-    const int a_rows = min(256, gt.size - 256 * tm), b_rows = min(256, N - (int)n0);
+    const int at = 256 * tm + (half > 0 ? 128 : 0);
+    const int64_t row0 = gt.row0 + at, n0 = 256 * tn;
+    const int a_rows = min(half < 0 ? 256 : 128, gt.size - at), b_rows = min(256, N - (int)n0);
+    if (a_rows <= 0) return;
     const PPOperand a{A + row0 * K, a_rows * K, K, sA + row0 * nk, a_rows * nk * 4, nk};
     const int b_blocks = b_rows / 128; // 1 in a last, half-empty tile column
     const PPOperand b{B + ((int64_t)gt.group * N + n0) * K, b_rows * K, K,
@@ -736,8 +741,9 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
     case kRows64x64: FP8Q_ROWS(4, 4, 4); break;
     default: {
         const int64_t tiles = max_tiles(a.rows, a.groups, 256) * ((a.N + 255) / 256);
-        grouped_pp_kernel<FA, FB><<<(unsigned)(tiles + kXcds), kBSThreads, 0, a.stream>>>(
-            a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C);
+        const int cus = a.cus / kXcds > 1 ? a.cus / kXcds : 1; // of an XCD
+        grouped_pp_kernel<FA, FB><<<(unsigned)(tiles + kXcds * (1 + cus / 2)), kBSThreads, 0, a.stream>>>(
+            a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C, cus);
     }
     }
 #undef FP8Q_ROWS
