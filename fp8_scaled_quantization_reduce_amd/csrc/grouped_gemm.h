@@ -478,7 +478,7 @@ template <int FA, int FB>
 __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,
     const float *__restrict__ sB, const int32_t *__restrict__ offsets, int groups, int rows, int M, int N,
-    int64_t stride, uint16_t *__restrict__ C)
+    int64_t stride, void *__restrict__ C)
 {
     constexpr int kTM = 256, kTN = 256;
     typedef PPShape<kTM> P;
@@ -498,21 +498,141 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
                       (a_rows * kbs - kb0) * 4, kbs};
     const PPOperand b{B + n0 * stride + (int64_t)kb0 * 128, b_rows * pitch - kb0 * 128, pitch, sB + n0 * kbs + kb0,
                       (b_rows * kbs - kb0) * 4, kbs};
-    uint16_t *c = C + ((int64_t)e * M + m0) * N + n0;
+    uint16_t *c = (uint16_t *)C + ((int64_t)e * M + m0) * N + n0;
     pp_tile<FA, FB, kTM, true>(st0, st1, sx, a, b, kbn, 0, c, N, a_rows, b_rows);
+}
+
+// A wave's 64 x 64 tile of a wgrad.  fp32 results (kWide): the codes are
+// widened to bf16 (exact) and multiplied by the bf16 matrix instruction, whose
+// sums are binary32.  The FP8 instruction adds the products of eight
+// neighbouring bytes on about 15 bits under the largest of them (measured on
+// the MI355X with one large and one small product at a time), which leaves an
+// fp32 result 1.1e-5 off in the 2-norm where the widened one is 7e-8 off: below
+// the rounding of a bf16 result, above that of an fp32 one.
+template <int FA, int FB, bool kWide> struct WgradWave {
+    v16f acc[2][2];
+    uint4 a[2][4], b[2][4]; // 32 rows x 128 K bytes each: chunks 4 fg .. 4 fg + 3 of row fr
+    bf16x8 aw[kWide ? 2 : 1][8];
+    int fr, fg;
+
+    __device__ __forceinline__ explicit WgradWave(int lane) : fr(lane & 31), fg(lane >> 5)
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    }
+    // step s of 16 K, widened
+    template <int F> __device__ __forceinline__ static bf16x8 step(const uint4 (&v)[4], int s)
+    {
+        const uint4 c = v[s >> 1];
+        return s & 1 ? widen8<F>((int)c.z, (int)c.w) : widen8<F>((int)c.x, (int)c.y);
+    }
+    __device__ __forceinline__ static v8i half(const uint4 (&v)[4], int s)
+    {
+        const uint4 lo = v[2 * s], hi = v[2 * s + 1];
+        return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    }
+    // all codes of a slice from the 64 rows at sa and at sb, so that the stage can be refilled
+    __device__ __forceinline__ void read(const uint8_t *sa, const uint8_t *sb)
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                a[i][c] = *reinterpret_cast<const uint4 *>(sa + swz(32 * i + fr, 4 * fg + c));
+                b[i][c] = *reinterpret_cast<const uint4 *>(sb + swz(32 * i + fr, 4 * fg + c));
+            }
+        if constexpr (kWide) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int s = 0; s < 8; ++s) aw[i][s] = step<FA>(a[i], s);
+        }
+    }
+    // the slice's products, weighted; runs of 16 rows' scales, 64 floats apart, at ga and gb
+    __device__ __forceinline__ void products(const float *ga, const float *gb)
+    {
+        float wi[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wi[i] = ga[64 * (2 * i + (fr >> 4)) + (fr & 15)];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            v16f p[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) p[i][r] = 0.0f;
+            if constexpr (kWide) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const bf16x8 bw = step<FB>(b[j], s);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        p[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw, aw[i][s], p[i], 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) p[i] = mfma32x32x64<FB, FA>(half(b[j], s), half(a[i], s), p[i]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v4f sb = *reinterpret_cast<const v4f *>(gb + 64 * (2 * j + (q >> 1)) + 8 * (q & 1) + 4 * fg);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j][4 * q + r] = __builtin_fmaf(p[i][4 * q + r], wi[i] * sb[r], acc[i][j][4 * q + r]);
+            }
+        }
+    }
+    // columns 8 q + 4 fg .. + 3 of row fr of the 32 x 32 tile (i, j)
+    __device__ __forceinline__ v4f quad(int i, int j, int q) const
+    {
+        return v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    }
+};
+
+// What the wgrad kernels below read of a tile: kTile rows of A and of B from
+// the first of the group's slices on, and their scales.
+struct WgradTile {
+    __amdgpu_buffer_rsrc_t a, b, sa, sb;
+    int pitch, s_pitch, slices;
+    int64_t row0, col0; // of C [groups * M][N]
+};
+
+// Block -> tile of kTile x kTile of a group's C; false: none.
+template <int kTile>
+__device__ __forceinline__ bool wgrad_tile(const uint8_t *A, const float *sA, const uint8_t *B, const float *sB,
+                                           const int32_t *offsets, int groups, int rows, int M, int N, int64_t stride,
+                                           WgradTile &t)
+{
+    const int tiles_m = M / kTile, tiles_n = N / kTile, per = tiles_m * tiles_n;
+    int e, tile, tm, tn, kb0;
+    group_share(blockIdx.x % kXcds, blockIdx.x / kXcds, per, e, tile);
+    if (e >= groups || tile >= per) return false;
+    group_tile(tile, tiles_m, tiles_n, tm, tn);
+    const int kbs = (int)(stride / 128), pitch = (int)stride;
+    group_blocks(offsets, groups, rows, e, kbs, kb0, t.slices);
+    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
+    const int bytes = kTile * pitch - kb0 * 128, s_bytes = (kTile * kbs - kb0) * 4;
+    t.a = __builtin_amdgcn_make_buffer_rsrc((void *)(A + m0 * stride + (int64_t)kb0 * 128), 0, bytes, kRawBufferWord3);
+    t.b = __builtin_amdgcn_make_buffer_rsrc((void *)(B + n0 * stride + (int64_t)kb0 * 128), 0, bytes, kRawBufferWord3);
+    t.sa = __builtin_amdgcn_make_buffer_rsrc((void *)(sA + m0 * kbs + kb0), 0, s_bytes, kRawBufferWord3);
+    t.sb = __builtin_amdgcn_make_buffer_rsrc((void *)(sB + n0 * kbs + kb0), 0, s_bytes, kRawBufferWord3);
+    t.pitch = pitch, t.s_pitch = kbs;
+    t.row0 = (int64_t)e * M + m0, t.col0 = n0;
+    return true;
 }
 
 // wgrad in 128 x 128 tiles, four waves of 64 x 64 per block, two blocks per
 // CU: one block's stores and first loads run beside the other's products.  A
 // wave reads its share of a slice from LDS into registers at once, so the
 // stage is free for the slice after next while the products run.
-//
-// fp32 results: the codes are widened to bf16 (exact) and multiplied by the
-// bf16 matrix instruction, whose sums are binary32.  The FP8 instruction adds
-// the products of eight neighbouring bytes on about 15 bits under the largest
-// of them (measured on the MI355X with one large and one small product at a
-// time), which leaves an fp32 result 1.1e-5 off in the 2-norm where the widened
-// one is 7e-8 off: below the rounding of a bf16 result, above that of an fp32 one.
 //
 // Eight 14336 x 4096 gradients over 8192 tokens, fp32: 1.20 ms, 0.80 PFLOP/s,
 // 1.9 GB written.  The chip's power bounds it: in 256 x 128 ping-pong tiles of
@@ -526,148 +646,60 @@ __global__ __launch_bounds__(256, 2) void grouped_wgrad_kernel(
     const float *__restrict__ sB, const int32_t *__restrict__ offsets, int groups, int rows, int M, int N,
     int64_t stride, void *__restrict__ C)
 {
-    constexpr bool kWide = DC == kF32;
     constexpr int kTile = 128, kOp = kTile * kBK, kSx = 16 * 64;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[2 * kOp];
     __shared__ __attribute__((aligned(1024))) uint8_t st1[2 * kOp];
     __shared__ __attribute__((aligned(16))) float sx0[kSx];
     __shared__ __attribute__((aligned(16))) float sx1[kSx];
-    const int tiles_m = M / kTile, tiles_n = N / kTile, per = tiles_m * tiles_n;
-    int e, tile, tm, tn, kb0, kbn;
-    group_share(blockIdx.x % kXcds, blockIdx.x / kXcds, per, e, tile);
-    if (e >= groups || tile >= per) return;
-    group_tile(tile, tiles_m, tiles_n, tm, tn);
-    const int kbs = (int)(stride / 128), pitch = (int)stride;
-    group_blocks(offsets, groups, rows, e, kbs, kb0, kbn);
-    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
+    WgradTile t;
+    if (!wgrad_tile<kTile>(A, sA, B, sB, offsets, groups, rows, M, N, stride, t)) return;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = w & 1, wn = w >> 1, fr = lane & 31, fg = lane >> 5;
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(A + m0 * stride + (int64_t)kb0 * 128), 0, kTile * pitch - kb0 * 128, kRawBufferWord3);
-    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(B + n0 * stride + (int64_t)kb0 * 128), 0, kTile * pitch - kb0 * 128, kRawBufferWord3);
-    const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc((void *)(sA + m0 * kbs + kb0), 0,
-                                                                         (kTile * kbs - kb0) * 4, kRawBufferWord3);
-    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc((void *)(sB + n0 * kbs + kb0), 0,
-                                                                         (kTile * kbs - kb0) * 4, kRawBufferWord3);
-    const int voff = (lane >> 3) * pitch + (((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) << 4);
-    const int svoff = ((lane & 15) * kbs + (lane >> 4)) * 4;
-
+    const int wm = w & 1, wn = w >> 1;
+    const int voff = (lane >> 3) * t.pitch + (((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) << 4);
+    const int svoff = ((lane & 15) * t.s_pitch + (lane >> 4)) * 4;
     // past the last slice the offset lies outside the buffer: nothing is read
     auto load = [&](uint8_t *st, int kb) {
-        const int at = kb < kbn ? kb * kBK : 1 << 30;
+        const int at = kb < t.slices ? kb * kBK : 1 << 30;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int row = 8 * (w + 4 * u);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(st + row * kBK), 16, voff, row * pitch + at, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(st + kOp + row * kBK), 16, voff, row * pitch + at,
-                                                     0, 0);
+            const int row = 8 * (w + 4 * u), off = row * t.pitch + at;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.a, (lds_void *)(st + row * kBK), 16, voff, off, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.b, (lds_void *)(st + kOp + row * kBK), 16, voff, off, 0, 0);
         }
     };
+    // scales of slices kb .. kb + 3, runs of 16 rows as [slice][row]
     auto load_scales = [&](float *sx, int kb) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int run = w + 4 * u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(sx + 64 * run), 4, svoff,
-                                                     (16 * run * kbs + kb) * 4, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(sx + 64 * (8 + run)), 4, svoff,
-                                                     (16 * run * kbs + kb) * 4, 0, 0);
+            const int run = w + 4 * u, off = (16 * run * t.s_pitch + kb) * 4;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.sa, (lds_void *)(sx + 64 * run), 4, svoff, off, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.sb, (lds_void *)(sx + 64 * (8 + run)), 4, svoff, off, 0, 0);
         }
     };
-    v16f acc[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-    // 32 rows x 128 K bytes: lane (fr, fg) takes chunks 4 fg .. 4 fg + 3 of row fr
-    auto read = [&](const uint8_t *st, int row, uint4(&o)[4]) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = *reinterpret_cast<const uint4 *>(st + swz(row + fr, 4 * fg + c));
-    };
-    // step s of 16 K, widened
-    auto step = [&](auto fmt, const uint4(&v)[4], int s) {
-        const uint4 c = v[s >> 1];
-        return s & 1 ? widen8<decltype(fmt)::value>((int)c.z, (int)c.w)
-                     : widen8<decltype(fmt)::value>((int)c.x, (int)c.y);
-    };
-    auto half = [&](const uint4(&v)[4], int s) {
-        const uint4 lo = v[2 * s], hi = v[2 * s + 1];
-        return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-    };
-    // one slice: all codes are read first, so that `then` can refill the stage
-    auto slice = [&](uint8_t *st, const float *sg, auto then) {
-        uint4 a[2][4], b[2][4];
-        float wi[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) read(st, wm * 64 + 32 * i, a[i]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) read(st + kOp, wn * 64 + 32 * j, b[j]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) wi[i] = sg[64 * (wm * 4 + 2 * i + (fr >> 4)) + (fr & 15)];
-        bf16x8 aw[kWide ? 2 : 1][8];
-        if constexpr (kWide) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int s = 0; s < 8; ++s) aw[i][s] = step(PhaseC<FA>{}, a[i], s);
-        }
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+    auto barrier = [&]() {
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        then();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            v16f p[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) p[i][r] = 0.0f;
-            if constexpr (kWide) {
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const bf16x8 bw = step(PhaseC<FB>{}, b[j], s);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        p[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bw, aw[i][s], p[i], 0, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        p[i] = mfma32x32x64<FB, FA>(half(b[j], s), half(a[i], s), p[i]);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const v4f sb = *reinterpret_cast<const v4f *>(sg + 64 * (8 + wn * 4 + 2 * j + (q >> 1)) +
-                                                              8 * (q & 1) + 4 * fg);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][4 * q + r] = __builtin_fmaf(p[i][4 * q + r], wi[i] * sb[r], acc[i][j][4 * q + r]);
-            }
-        }
     };
+    WgradWave<FA, FB, DC == kF32> tile(lane);
     load_scales(sx0, 0);
     load(st0, 0);
     load(st1, 1);
     for (int kb = 0;; kb += 8) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if (kb + u >= kbn) goto done;
+            if (kb + u >= t.slices) goto done;
+            uint8_t *st = u & 1 ? st1 : st0;
+            const float *sg = (u & 4 ? sx1 : sx0) + 16 * (u & 3);
             // this slice's loads have landed; the next one's (and the scales) may be in flight
             if ((u & 3) == 1) __builtin_amdgcn_s_waitcnt(waitcnt_imm(12, 15));
             else __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 15));
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            slice(u & 1 ? st1 : st0, (u & 4 ? sx1 : sx0) + 16 * (u & 3), [&]() {
-                if ((u & 3) == 0) load_scales(u & 4 ? sx0 : sx1, kb + u + 4);
-                load(u & 1 ? st1 : st0, kb + u + 2);
-            });
+            barrier();
+            tile.read(st + wm * 64 * kBK, st + kOp + wn * 64 * kBK);
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            barrier(); // every wave has read the stage
+            if ((u & 3) == 0) load_scales(u & 4 ? sx0 : sx1, kb + u + 4);
+            load(st, kb + u + 2);
+            tile.products(sg + 64 * 4 * wm, sg + 64 * (8 + 4 * wn));
         }
     }
 done:
@@ -675,21 +707,108 @@ done:
     __syncthreads();
     // each wave stages its 64 x 64 results and stores whole row pieces
     typedef EpiStage<64, DC == kF32 ? 4 : 2, 64, 16384> ES;
+    uint8_t *ep = (w < 2 ? st0 : st1) + (w & 1) * 16384;
     uint32_t m = 0;
     const Epi none{nullptr, kActNone, nullptr};
-    uint8_t *ep = (w < 2 ? st0 : st1) + (w & 1) * 16384;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const v4f v{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                ES::put(ep, 32 * i + fr, 8 * j + 2 * q + fg,
-                        pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, v, m, none, 0.0f));
-            }
+            for (int q = 0; q < 4; ++q)
+                ES::put(ep, 32 * i + tile.fr, 8 * j + 2 * q + tile.fg,
+                        pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, tile.quad(i, j, q), m, none, 0.0f));
     __syncthreads();
-    ES::store(ep, C, N, (int64_t)e * M + m0 + wm * 64, n0 + wn * 64, lane);
+    ES::store(ep, C, N, t.row0 + wm * 64, t.col0 + wn * 64, lane);
+}
+
+// wgrad of few tiles: a 64 x 64 tile of one group's C per block, whose four
+// waves take a quarter of the group's slices each, from stages of their own
+// (no barrier until the end), and add their sums through LDS in a fixed order.
+template <int FA, int FB, int DC>
+__global__ __launch_bounds__(256, 1) void grouped_wgrad_split_kernel(
+    const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,
+    const float *__restrict__ sB, const int32_t *__restrict__ offsets, int groups, int rows, int M, int N,
+    int64_t stride, void *__restrict__ C)
+{
+    constexpr int kTile = 64, kOp = kTile * kBK, kSx = 8 * 64;
+    __shared__ __attribute__((aligned(1024))) uint8_t st0s[4][2 * kOp];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1s[4][2 * kOp];
+    __shared__ __attribute__((aligned(16))) float sx0s[4][kSx];
+    __shared__ __attribute__((aligned(16))) float sx1s[4][kSx];
+    WgradTile t;
+    if (!wgrad_tile<kTile>(A, sA, B, sB, offsets, groups, rows, M, N, stride, t)) return;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int each = (t.slices + 3) / 4, k0 = w * each, kn = min(each, t.slices - k0);
+    uint8_t *st0 = st0s[w], *st1 = st1s[w];
+    float *sx0 = sx0s[w], *sx1 = sx1s[w];
+    int voff[2]; // rows 8 u + lane / 8, u even and odd
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        voff[u] = (lane >> 3) * t.pitch + (((lane & 7) ^ ((4 * u + (lane >> 4)) & 7)) << 4);
+    const int svoff = ((lane & 15) * t.s_pitch + (lane >> 4)) * 4;
+    auto load = [&](uint8_t *st, int k) {
+        const int at = k < kn ? (k0 + k) * kBK : 1 << 30;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int row = 8 * u, off = row * t.pitch + at;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.a, (lds_void *)(st + row * kBK), 16, voff[u & 1], off, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.b, (lds_void *)(st + kOp + row * kBK), 16, voff[u & 1], off, 0, 0);
+        }
+    };
+    auto load_scales = [&](float *sx, int k) {
+#pragma unroll
+        for (int run = 0; run < 4; ++run) {
+            const int off = (16 * run * t.s_pitch + k0 + k) * 4;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.sa, (lds_void *)(sx + 64 * run), 4, svoff, off, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(t.sb, (lds_void *)(sx + 64 * (4 + run)), 4, svoff, off, 0, 0);
+        }
+    };
+    WgradWave<FA, FB, DC == kF32> tile(lane);
+    load_scales(sx0, 0);
+    load(st0, 0);
+    load(st1, 1);
+    for (int kb = 0;; kb += 8) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (kb + u >= kn) goto done;
+            uint8_t *st = u & 1 ? st1 : st0;
+            const float *sg = (u & 4 ? sx1 : sx0) + 16 * (u & 3);
+            if ((u & 3) == 1) __builtin_amdgcn_s_waitcnt(waitcnt_imm(24, 15));
+            else __builtin_amdgcn_s_waitcnt(waitcnt_imm(16, 15));
+            asm volatile("" ::: "memory");
+            tile.read(st, st + kOp);
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            asm volatile("" ::: "memory");
+            if ((u & 3) == 0) load_scales(u & 4 ? sx0 : sx1, kb + u + 4);
+            load(st, kb + u + 2);
+            tile.products(sg, sg + 64 * 4);
+        }
+    }
+done:
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    // wave w adds and stores the 32 x 32 tile (w / 2, w % 2)
+    v4f(*sums)[64] = reinterpret_cast<v4f(*)[64]>(st0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sums[(2 * i + j) * 4 + q][lane] = tile.quad(i, j, q);
+    __syncthreads();
+    typedef EpiStage<32, DC == kF32 ? 4 : 2, 32, 4096> ES;
+    uint32_t m = 0;
+    const Epi none{nullptr, kActNone, nullptr};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v4f c{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c += reinterpret_cast<const v4f(*)[64]>(st0s[k])[4 * w + q][lane];
+        ES::put(st1, tile.fr, 2 * q + tile.fg,
+                pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, c, m, none, 0.0f));
+    }
+    __syncthreads();
+    ES::store(st1, C, N, t.row0 + 32 * (w >> 1), t.col0 + 32 * (w & 1), lane);
 }
 
 // The tile of an fprop / dgrad launch.  Up to 12 rows a group on average most
@@ -750,20 +869,31 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
     return hipGetLastError();
 }
 
-// The tile of a bf16 wgrad launch, from the time of a round of one 256 x 256
-// tile or two 128 x 128 tiles per CU, in us, s slices of 128 tokens per group on
-// average (eight 4096 x 4096 gradients, 1 to 32 slices: 83 to 570 us in the
-// large tiles, 82 to 730 us in the small ones).  The large tiles reuse what they
-// read more, the small ones fill the chip where there are few: one 1408 x 2048
-// gradient over 32768 tokens 211 us, in large tiles 370 us.
-inline bool wgrad_large_tiles(const GroupedArgs &a)
+// The tiles of a wgrad launch, from the time of a round of blocks in us with s
+// slices of 128 tokens per group on average.  Measured on one to sixteen
+// gradients of 768 x 1152 to 4096 x 4096 with 1 to 128 slices: 256 x 256 (bf16
+// only) 8.5 + 1.9 s per tile and CU, 128 x 128 5 + 1.3 s per two tiles and CU
+// (0.8 s where there is one; fp32 2.0 and 1.1), split 64 x 64 5 + 0.25 s per
+// tile and CU (fp32 0.31).  The large tiles reuse most of what they read, the
+// small ones fill the chip where there are few: one 768 x 1152 gradient over
+// 16384 tokens 184, 93 and 36 us (bf16), eight 4096 x 4096 over 32768 548, 711
+// and more.
+enum WgradTiles { kWgradSplit, kWgradSmall, kWgradLarge };
+
+inline WgradTiles wgrad_tiles(const GroupedArgs &a)
 {
     const int64_t cus = a.cus > 0 ? a.cus : 256;
-    auto rounds = [&](int tile, int64_t wide) {
-        return (double)((a.groups * ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile) + wide - 1) / wide);
-    };
+    auto tiles = [&](int tile) { return a.groups * ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile); };
+    auto up = [](int64_t n, int64_t d) { return (double)((n + d - 1) / d); };
     const double s = (double)a.rows / 128.0 / a.groups;
-    return rounds(256, cus) * (8.5 + 1.9 * s) <= rounds(128, 2 * cus) * (3.9 + 1.3 * s);
+    const bool bf16 = a.c_dtype == kBF16;
+    const int64_t small = tiles(128), last = small % (2 * cus);
+    const double two = 5.0 + (bf16 ? 1.3 : 2.0) * s, one = 5.0 + (bf16 ? 0.8 : 1.1) * s;
+    const double us_small = (double)(small / (2 * cus)) * two + (last == 0 ? 0.0 : last <= cus ? one : two);
+    const double us_split = up(tiles(64), cus) * (5.0 + (bf16 ? 0.25 : 0.31) * s);
+    const double us_large = up(tiles(256), cus) * (8.5 + 1.9 * s);
+    if (us_split < us_small && !(bf16 && us_large < us_split)) return kWgradSplit;
+    return bf16 && us_large <= us_small ? kWgradLarge : kWgradSmall;
 }
 
 template <int FA, int FB> hipError_t launch_grouped_wgrad(const GroupedArgs &a)
@@ -772,14 +902,22 @@ template <int FA, int FB> hipError_t launch_grouped_wgrad(const GroupedArgs &a)
         const int64_t per = ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile);
         return (unsigned)(a.groups * (int64_t)kXcds * ((per + kXcds - 1) / kXcds));
     };
-    if (a.c_dtype == kBF16 && wgrad_large_tiles(a)) {
-        grouped_wgrad_pp_kernel<FA, FB><<<grid(256), kBSThreads, 0, a.stream>>>(
-            a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N, a.stride, (uint16_t *)a.C);
-    } else {
-        auto k = a.c_dtype == kBF16 ? grouped_wgrad_kernel<FA, FB, kBF16> : grouped_wgrad_kernel<FA, FB, kF32>;
-        k<<<grid(128), 256, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N,
-                                           a.stride, a.C);
+    const bool bf16 = a.c_dtype == kBF16;
+#define FP8Q_WGRAD(TILE, THREADS, K)                                                                                 \
+    K<<<grid(TILE), THREADS, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N,  \
+                                            a.stride, a.C)
+    switch (wgrad_tiles(a)) {
+    case kWgradLarge: FP8Q_WGRAD(256, kBSThreads, (grouped_wgrad_pp_kernel<FA, FB>)); break;
+    case kWgradSmall:
+        if (bf16) FP8Q_WGRAD(128, 256, (grouped_wgrad_kernel<FA, FB, kBF16>));
+        else FP8Q_WGRAD(128, 256, (grouped_wgrad_kernel<FA, FB, kF32>));
+        break;
+    case kWgradSplit:
+        if (bf16) FP8Q_WGRAD(64, 256, (grouped_wgrad_split_kernel<FA, FB, kBF16>));
+        else FP8Q_WGRAD(64, 256, (grouped_wgrad_split_kernel<FA, FB, kF32>));
+        break;
     }
+#undef FP8Q_WGRAD
     return hipGetLastError();
 }
 

@@ -201,3 +201,30 @@ def test_clip_past_2_31_elements():
     for i, v in ((0, 2.0 ** -10), (n // 2, 2.0 ** -10), (n - 2, 2.0 ** -10), (n - 1, 3.0), ((1 << 31) + 5, -5.0)):
         assert abs(float(g[i]) - v * c) <= 2.0 ** -8 * abs(v * c) * (1 + 1e-3)
     assert int((g == g[0]).sum()) == n - 2
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [[2000], [0, 1500, 130], [128 * 13], [700, 1, 900, 4000], [127 + 128 * 8]])
+def test_wgrad_of_few_tiles(sizes, dtype):
+    """Few tiles over many slices: quarters of the contraction of equal and of
+    unequal length, empty ones among them."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    pad = np.concatenate([[0], np.cumsum((np.asarray(sizes) + 127) // 128 * 128)])
+    for m, n in ((128, 128), (384, 256)):
+        tp = int(pad[-1]) + 128
+        a, sa, b, sb = codes(gen, m, tp), scales(gen, m, tp // 128), codes(gen, n, tp), scales(gen, n, tp // 128)
+        buf = torch.full((len(sizes) * m * n + 256,), 7.0, dtype=dtype, device="cuda")
+        c = buf[128:-128].view(len(sizes), m, n)
+        fq.fp8_grouped_gemm_wgrad(a, E5, sa, b, E4, sb, offsets(sizes), c)
+        wa = value(a, E5) * np.repeat(host(sa).astype(np.float64), 128, 1)
+        wb = value(b, E4) * np.repeat(host(sb).astype(np.float64), 128, 1)
+        for e in range(len(sizes)):
+            lo, hi = int(pad[e]), int(pad[e + 1])
+            if lo == hi:
+                assert not c[e].any()
+            else:
+                close(c[e], wa[:, lo:hi], wb[:, lo:hi], hi - lo, dtype == torch.bfloat16)
+        assert torch.all(buf[:128] == 7.0) and torch.all(buf[-128:] == 7.0)
+        again = torch.empty_like(c)
+        fq.fp8_grouped_gemm_wgrad(a, E5, sa, b, E4, sb, offsets(sizes), again)
+        assert torch.equal(c, again)
