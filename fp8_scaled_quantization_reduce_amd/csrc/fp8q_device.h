@@ -121,6 +121,12 @@ __device__ __forceinline__ void st_stream(void *p, uint4 v)
     __builtin_nontemporal_store(u32x4v{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4v *>(p));
 }
 
+__device__ __forceinline__ void st_stream(void *p, uint2 v)
+{
+    typedef unsigned int u32x2v __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(u32x2v{v.x, v.y}, reinterpret_cast<u32x2v *>(p));
+}
+
 __device__ __forceinline__ uint32_t ld_stream_u32(const void *p)
 {
     return __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(p));

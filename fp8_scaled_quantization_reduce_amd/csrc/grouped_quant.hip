@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kGqThreads) void rows_kernel(const typename In<DT>:
                     o.x = encode4<F>(v[k][0], v[k][1], v[k][2], v[k][3], sc.scale);
                     o.y = encode4<F>(v[k][4], v[k][5], v[k][6], v[k][7], sc.scale);
                 }
-                *reinterpret_cast<uint2 *>(q + (t0 + k) * cols + c) = o;
+                st_stream(q + (t0 + k) * cols + c, o);
                 if ((lane & 15) == 0) s[(t0 + k) * (cols / 128) + c / 128] = sc.s;
             }
         }
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(kGqThreads, 4) void tile_both_kernel(
             }
             if (r < live) {
                 const int64_t row = (int64_t)gt.row0 + first + r;
-                *reinterpret_cast<uint4 *>(q_row + row * cols + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+                st_stream(q_row + row * cols + c0, make_uint4(o[0], o[1], o[2], o[3]));
                 if (jg == 0) s_row[row * blocks_c + cb] = sc.s;
             }
         }

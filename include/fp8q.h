@@ -559,7 +559,7 @@ int fp8q_layernorm_backward_workspace(int32_t dtype, int64_t rows, int64_t cols,
  *   g      HOST array of `count` device pointers; tensor i has n[i] >= 0
  *          elements of dtype[i] (host arrays too), aligned to its elements
  *   out    HOST array of device pointers of the same sizes and types, each
- *          equal to g[i] or not overlapping it; NULL: in place
+ *          equal to g[i] or overlapping no gradient; NULL: in place
  *   max_norm  not negative; +inf: only norm (and coef = 1) are computed, and
  *          out must be NULL
  *   norm, coef  one device float each
