@@ -65,6 +65,9 @@ struct GroupedArgs {
 // counts: 16 kMT rows of a group x 16 kNT columns per block, fragments loaded
 // straight from memory into registers (a weight byte is used by one wave).
 // kWK waves take the 128-wide slices in turn and add their sums through LDS.
+// The weights' bytes bound it: 64 rows over eight 14336 x 4096 matrices 86 us,
+// 5.5 TB/s; the hint that a weight is read once costs 15%, loads of two or four
+// slices at a time change nothing.
 template <int FA, int FB, int kMT, int kNT, int kWK>
 __global__ __launch_bounds__(64 * kWK) void grouped_rows_kernel(const uint8_t *__restrict__ A,
                                                                 const float *__restrict__ sA,
@@ -854,7 +857,14 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
             a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C)
     switch (rows_tile(a)) {
     case kRows16x16: FP8Q_ROWS(1, 1, 8); break;
-    case kRows16x32: FP8Q_ROWS(1, 2, 8); break;
+    case kRows16x32:
+        // one to four slices a wave: 64 rows over eight 8192-column matrices in
+        // us with 4, 8 and 16 waves: K 1024 13.6, 15.8, 18.9; 3456 44.5, 43.3,
+        // 47.0; 4096 54.4, 53.8, 52.3; 7168 88.1, 87.8, 86.6
+        if (a.K < 2048) FP8Q_ROWS(1, 2, 4);
+        else if (a.K < 4096) FP8Q_ROWS(1, 2, 8);
+        else FP8Q_ROWS(1, 2, 16);
+        break;
     case kRows32x32: FP8Q_ROWS(2, 2, 8); break;
     case kRows32x64: FP8Q_ROWS(2, 4, 4); break;
     case kRows64x64: FP8Q_ROWS(4, 4, 4); break;

@@ -228,3 +228,10 @@ def test_wgrad_of_few_tiles(sizes, dtype):
         again = torch.empty_like(c)
         fq.fp8_grouped_gemm_wgrad(a, E5, sa, b, E4, sb, offsets(sizes), again)
         assert torch.equal(c, again)
+
+
+@pytest.mark.parametrize("k", [128, 384, 1920, 2048, 3968, 4096, 4224])
+def test_gemm_few_rows_over_long_contractions(k):
+    """Fewer, as many and more slices than the waves that share a tile's contraction."""
+    sizes = [1, 0, 9, 16, 17, 3] * 4
+    check_rows(sizes, 2048, k, np.arange(sum(sizes)), np.arange(0, 2048, 3))
