@@ -400,7 +400,13 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
 // fprop / dgrad in tiles of 256 rows x 256 columns; a group's last tile of at
 // most 128 rows runs as a 128 x 256 tile.  Each XCD has a contiguous run of
 // the tiles; what it leaves for a last round on at most half of its CUs runs as
-// two 128 x 256 tiles each.
+// two 128 x 256 tiles each (9000 rows of three 2048 x 2048 matrices 54.6 -> 49.1 us).
+//
+// Long contractions are bound by the card's power: 16384 rows over eight
+// 14336 x 4096 matrices 0.90 ms, 2.14 PFLOP/s at 1.7 GHz.  A tile also takes 6
+// us beside its slices (1.9 us each with the chip full): finding its group,
+// the first loads, the stores; 24594 rows over 64 matrices of 2048 x 1408, 11
+// slices, 108 us, 1.3 PFLOP/s.
 template <int FA, int FB>
 __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t *__restrict__ A,
                                                                    const float *__restrict__ sA,
@@ -476,7 +482,12 @@ __device__ __forceinline__ void group_share(int xcd, int i, int per, int &e, int
     tile = xcd * share + j;
 }
 
-// wgrad with bf16 results in 256 x 256 tiles of one group's C.
+// wgrad with bf16 results in 256 x 256 tiles of one group's C.  Every result
+// takes a multiply and a multiply-add of scales per slice, which the wave that
+// runs its products issues too: 1.9 us a slice against 0.9 of the matrix
+// unit, and 8.5 us a tile for the rest.  24594 tokens, 64 gradients of 1408 x
+// 2048: 187 us, 0.76 PFLOP/s; eight of 4096 x 4096 over 32768 tokens 560 us,
+// 1.97 PFLOP/s.
 template <int FA, int FB>
 __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,
@@ -637,7 +648,7 @@ __device__ __forceinline__ bool wgrad_tile(const uint8_t *A, const float *sA, co
 // wave reads its share of a slice from LDS into registers at once, so the
 // stage is free for the slice after next while the products run.
 //
-// Eight 14336 x 4096 gradients over 8192 tokens, fp32: 1.20 ms, 0.80 PFLOP/s,
+// Eight 14336 x 4096 gradients over 8192 tokens, fp32: 1.16 ms, 0.83 PFLOP/s,
 // 1.9 GB written.  The chip's power bounds it: in 256 x 128 ping-pong tiles of
 // one block per CU the same work took 30% more cycles at a 25% higher clock
 // (2.91 million at 2.25 GHz, here 2.23 at 1.78).  Without the loads of the

@@ -130,6 +130,8 @@ template <int R, int kV, bool kFull> struct Cols {
 
 // Each R-lane team walks its share of the rows: the next row is fetched before
 // the row in hand is reduced, and (kHeld) the gain and bias stay in registers.
+// Memory bounds it: 16384x4096 bf16 51.5 us, 5.2 TB/s (63 us without the row
+// ahead); 2051x5003 fp32 16.8 us, 4.9 TB/s; one row of 4096 2.7 us, its launch.
 template <int DT, int PT, int R, int kI, bool kFull>
 __global__ __launch_bounds__(R > kLnThreads ? R : kLnThreads) void ln_fwd_kernel(
     const typename Elem<DT>::type *__restrict__ x, int64_t rows, int64_t cols_,
