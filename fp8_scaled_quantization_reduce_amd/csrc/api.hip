@@ -1199,8 +1199,8 @@ static int fp8_grouped_gemm_impl(const uint8_t *A, int32_t fa, const float *sA, 
     if (st) return st;
     if (N < 0 || K < 0) return fail(FP8Q_EINVAL, "%s: negative shape", fn);
     if (N % 128 || K % 128) return fail(FP8Q_EUNSUPPORTED, "%s: N and K must be multiples of 128", fn);
-    if (K > (int64_t)1 << 22 || N > (int64_t)1 << 24)
-        return fail(FP8Q_EUNSUPPORTED, "%s: K exceeds 2^22 or N 2^24", fn);
+    if (K > (int64_t)1 << 22 || N > (int64_t)1 << 23)
+        return fail(FP8Q_EUNSUPPORTED, "%s: K exceeds 2^22 or N 2^23", fn);
     if ((rows / 16 + groups) * (N / 16) > 0x7FFFFFFF) return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^31 tiles", fn);
     const void *in[5] = {A, B, sA, sB, offsets};
     const int64_t bytes[5] = {rows * K, groups * N * K, rows * (K / 128) * 4, groups * (N / 128) * (K / 128) * 4,
@@ -1233,8 +1233,8 @@ static int fp8_grouped_gemm_wgrad_impl(const uint8_t *A, int32_t fa, const float
     if (M < 0 || N < 0) return fail(FP8Q_EINVAL, "%s: negative shape", fn);
     if (M % 128 || N % 128) return fail(FP8Q_EUNSUPPORTED, "%s: M and N must be multiples of 128", fn);
     if (col_stride < 0 || col_stride % 128) return fail(FP8Q_EINVAL, "%s: col_stride must be a multiple of 128", fn);
-    if (col_stride > (int64_t)1 << 22 || M > (int64_t)1 << 24 || N > (int64_t)1 << 24)
-        return fail(FP8Q_EUNSUPPORTED, "%s: col_stride exceeds 2^22 or M or N 2^24", fn);
+    if (col_stride > (int64_t)1 << 22 || M > (int64_t)1 << 23 || N > (int64_t)1 << 23)
+        return fail(FP8Q_EUNSUPPORTED, "%s: col_stride exceeds 2^22 or M or N 2^23", fn);
     if (groups * (M / 64) * (N / 64) > 0x7FFFFFFF) return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^31 tiles", fn);
     const void *in[5] = {A, B, sA, sB, offsets};
     const int64_t bytes[5] = {M * col_stride, N * col_stride, M * (col_stride / 128) * 4, N * (col_stride / 128) * 4,

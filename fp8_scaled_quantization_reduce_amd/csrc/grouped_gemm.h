@@ -48,6 +48,8 @@ template <int F> __device__ __forceinline__ bf16x8 widen8(int lo, int hi)
     return bf16x8{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
 }
 
+constexpr int kBufferNt = 2; // the non-temporal hint of a buffer store
+
 struct GroupedArgs {
     const uint8_t *A, *B;
     const float *sA, *sB;
@@ -363,37 +365,32 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 
-    // epilogue: each wave stages its 64 x kWC results and stores whole row pieces
+    // epilogue: each wave stages its 64 x kWC results in a part of the stages of
+    // its own and stores whole row pieces (rows past the tile's own lie outside
+    // the buffer and are dropped)
     typedef EpiStage<P::kWC, 2, 64, P::kWC * kBK> ES;
+    static_assert(ES::kPasses == 1, "a wave's results fit its part of the stages");
     const int wrow = wm * 64, wcol = wn * P::kWC;
-    const bool inside = wrow < c_rows && wcol < c_cols;
+    if (wrow >= c_rows || wcol >= c_cols) return;
     uint8_t *ep = (w < 4 ? st0 : st1) + (w & 3) * (P::kWC * kBK);
     uint32_t m = 0;
     const Epi none{nullptr, kActNone, nullptr};
 #pragma unroll
-    for (int ps = 0; ps < ES::kPasses; ++ps) {
-        if (ps > 0) __syncthreads();
-        if (inside) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if ((16 * i) / ES::kPassRows != ps) continue;
-#pragma unroll
-                for (int j = 0; j < 2 * kJT; ++j)
-                    ES::put(ep, 16 * i + fr - ps * ES::kPassRows, 4 * j + fg,
-                            pack_out4<kOutBF16, false, false>(0, acc[i][j], m, none, 0.0f));
-            }
-        }
-        __syncthreads();
-        if (inside) {
-            const int c = lane % ES::kNC, rr = lane / ES::kNC;
-            uint8_t *Cb = reinterpret_cast<uint8_t *>(C);
+        for (int j = 0; j < 2 * kJT; ++j)
+            ES::put(ep, 16 * i + fr, 4 * j + fg, pack_out4<kOutBF16, false, false>(0, acc[i][j], m, none, 0.0f));
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+    asm volatile("" ::: "memory");
+    const int pitch = (int)ldc * 2, left = min(64, c_rows - wrow);
+    const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(C + (int64_t)wrow * ldc + wcol), 0, (left - 1) * pitch + P::kWC * 2, kRawBufferWord3);
+    const int c = lane % ES::kNC, rr = lane / ES::kNC, voff = rr * pitch + 16 * c;
 #pragma unroll 4
-            for (int s = 0; s < ES::kPassRows / ES::kRowsPerStore; ++s) {
-                const int r = s * ES::kRowsPerStore + rr, row = wrow + ps * ES::kPassRows + r;
-                const uint4 v = *reinterpret_cast<const uint4 *>(ep + ES::addr(r, c));
-                if (row < c_rows) st_stream(Cb + ((int64_t)row * ldc + wcol) * 2 + 16 * c, v);
-            }
-        }
+    for (int s = 0; s < 64 / ES::kRowsPerStore; ++s) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(ep + ES::addr(s * ES::kRowsPerStore + rr, c));
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4v{v.x, v.y, v.z, v.w}, rc, voff, s * ES::kRowsPerStore * pitch,
+                                                   kBufferNt);
     }
 }
 
@@ -449,37 +446,61 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_pp_kernel(const uint8_t
         pp_tile<FA, FB, 128, false>(st0, st1, sx, a, b, nk, b_blocks - 1, c, N, a_rows, b_rows);
 }
 
-// Blocks of 128 tokens before group e and in it (wave-uniform).
-__device__ __forceinline__ void group_blocks(const int32_t *offsets, int groups, int rows, int e, int kbs, int &kb0,
-                                             int &kbn)
-{
-    kb0 = kbn = 0;
-    for (int g0 = 0; g0 <= e; g0 += 64) {
+// The groups' blocks of 128 tokens, 64 groups at a time in a wave's lanes.
+struct GroupBlocks {
+    const int32_t *offsets;
+    int groups, rows;
+    int count, sum; // blocks of group 64 i + lane and inclusive sums, for the chunk held
+
+    __device__ __forceinline__ void hold(int g0)
+    {
         int lo, size;
         group_rows(offsets, groups, rows, g0 + (threadIdx.x & 63), lo, size);
-        const int count = (int)(((unsigned)size + 127) / 128), sum = wave_scan_i32(count);
-        if (e < g0 + 64) {
-            kbn = __builtin_amdgcn_readlane(count, e - g0);
-            kb0 += __builtin_amdgcn_readlane(sum, e - g0) - kbn;
-        } else {
+        count = (int)(((unsigned)size + 127) / 128);
+        sum = wave_scan_i32(count);
+    }
+    // chunk 0 is read first: the loads run beside the search for the tile
+    __device__ __forceinline__ GroupBlocks(const int32_t *o, int g, int r) : offsets(o), groups(g), rows(r) { hold(0); }
+
+    // The group that comes i-th: those with more than the average first, so
+    // that the launch does not end on the longest tiles (up to 64 groups).
+    __device__ __forceinline__ int ordered(int i) const
+    {
+        if (groups > 64) return i;
+        const int lane = threadIdx.x & 63, total = __builtin_amdgcn_readlane(sum, 63);
+        const bool live = lane < groups, big = live && (int64_t)count * groups > total;
+        const uint64_t bigs = __ballot(big), rest = __ballot(live && !big);
+        const uint64_t mine = big ? bigs : rest;
+        const int before = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mine >> 32),
+                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)mine, 0));
+        const int rank = live ? before + (big ? 0 : __popcll(bigs)) : 64;
+        return __ffsll((unsigned long long)__ballot(rank == i)) - 1;
+    }
+    // blocks before group e and in it (wave-uniform), clipped to the kbs that the operands hold
+    __device__ __forceinline__ void find(int e, int kbs, int &kb0, int &kbn)
+    {
+        kb0 = 0;
+        for (int g0 = 0;; g0 += 64) {
+            if (g0 > 0) hold(g0);
+            if (e < g0 + 64) break;
             kb0 += __builtin_amdgcn_readlane(sum, 63);
         }
+        kbn = __builtin_amdgcn_readlane(count, e & 63);
+        kb0 += __builtin_amdgcn_readlane(sum, e & 63) - kbn;
+        kb0 = min(kb0, kbs);
+        kbn = min(kbn, kbs - kb0);
     }
-    // the caller's buffers may be too short for these offsets
-    kb0 = min(kb0, kbs);
-    kbn = min(kbn, kbs - kb0);
-}
+};
 
 // Tile i of an XCD's share of the groups' tiles (`per` each): every group's
 // tiles are split over the XCDs, so that they get equal shares of long and of
 // short contractions; an XCD's share of a group is a contiguous run of its
-// grouped order.  tile >= per: none.
+// grouped order.  e: place of the group; tile >= per: none.
 __device__ __forceinline__ void group_share(int xcd, int i, int per, int &e, int &tile)
 {
     const int share = (per + kXcds - 1) / kXcds;
-    e = i / share;
-    const int j = i - e * share;
-    tile = xcd * share + j;
+    e = (int)((unsigned)i / (unsigned)share);
+    tile = xcd * share + (i - e * share);
 }
 
 // wgrad with bf16 results in 256 x 256 tiles of one group's C.  Every result
@@ -501,11 +522,13 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     __shared__ __attribute__((aligned(16))) float sx[kScaleGroups * 64 * pp_scale_runs<kTM, true>()];
     const int tiles_m = (M + kTM - 1) / kTM, tiles_n = (N + kTN - 1) / kTN, per = tiles_m * tiles_n;
     int e, tile, tm, tn, kb0, kbn;
+    GroupBlocks blocks(offsets, groups, rows);
     group_share(blockIdx.x % kXcds, blockIdx.x / kXcds, per, e, tile);
     if (e >= groups || tile >= per) return;
     group_tile(tile, tiles_m, tiles_n, tm, tn);
     const int kbs = (int)(stride / 128);
-    group_blocks(offsets, groups, rows, e, kbs, kb0, kbn);
+    e = blocks.ordered(e);
+    blocks.find(e, kbs, kb0, kbn);
     const int64_t m0 = (int64_t)tm * kTM, n0 = (int64_t)tn * kTN;
     const int a_rows = min(kTM, M - (int)m0), b_rows = min(kTN, N - (int)n0), pitch = (int)stride;
     const PPOperand a{A + m0 * stride + (int64_t)kb0 * 128, a_rows * pitch - kb0 * 128, pitch, sA + m0 * kbs + kb0,
@@ -627,11 +650,13 @@ __device__ __forceinline__ bool wgrad_tile(const uint8_t *A, const float *sA, co
 {
     const int tiles_m = M / kTile, tiles_n = N / kTile, per = tiles_m * tiles_n;
     int e, tile, tm, tn, kb0;
+    GroupBlocks blocks(offsets, groups, rows);
     group_share(blockIdx.x % kXcds, blockIdx.x / kXcds, per, e, tile);
     if (e >= groups || tile >= per) return false;
     group_tile(tile, tiles_m, tiles_n, tm, tn);
     const int kbs = (int)(stride / 128), pitch = (int)stride;
-    group_blocks(offsets, groups, rows, e, kbs, kb0, t.slices);
+    e = blocks.ordered(e);
+    blocks.find(e, kbs, kb0, t.slices);
     const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
     const int bytes = kTile * pitch - kb0 * 128, s_bytes = (kTile * kbs - kb0) * 4;
     t.a = __builtin_amdgcn_make_buffer_rsrc((void *)(A + m0 * stride + (int64_t)kb0 * 128), 0, bytes, kRawBufferWord3);

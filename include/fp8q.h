@@ -479,7 +479,8 @@ int fp8_quantize_grouped(const void *x, int32_t dtype, int64_t x_rows, int64_t c
  *      blocks, as fp8_quantize_block writes them group by group)
  *   C  [rows][N] bf16
  * with the arithmetic of fp8_scaled_gemm(FP8Q_BLOCK_1x128_128x128).  Groups
- * may have any number of rows; N and K are multiples of 128 (K at most 2^22).
+ * may have any number of rows; N and K are multiples of 128 (K at most 2^22,
+ * N at most 2^23).
  */
 int fp8_grouped_gemm(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb, const float *sB,
                      const int32_t *offsets, int32_t groups, int64_t rows, int64_t N, int64_t K, void *C,
@@ -500,7 +501,7 @@ int fp8_grouped_gemm(const uint8_t *A, int32_t fa, const float *sA, const uint8_
  * widened to bf16 (exactly) for the bf16 matrix instruction, whose sums are
  * binary32: the FP8 instruction adds neighbouring products on about 15 bits,
  * which an fp32 gradient would show (1.1e-5 in the 2-norm).
- * M and N are multiples of 128, col_stride at most 2^22.
+ * M and N are multiples of 128 and at most 2^23, col_stride at most 2^22.
  */
 int fp8_grouped_gemm_wgrad(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb,
                            const float *sB, const int32_t *offsets, int32_t groups, int64_t rows, int64_t col_stride,
