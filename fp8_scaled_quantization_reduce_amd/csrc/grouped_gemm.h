@@ -141,6 +141,26 @@ __global__ __launch_bounds__(64 * kWK) void grouped_rows_kernel(const uint8_t *_
     }
 }
 
+// A wave's staged results (kRows rows of `bytes` bytes) to C, rows `pitch` bytes
+// apart; rows from `left` on lie outside the buffer and are dropped.  The wave
+// wrote the stage itself, so it waits for no other.
+template <typename ES, int kRows>
+__device__ __forceinline__ void store_rows(const uint8_t *ep, void *C, int pitch, int bytes, int left, int lane)
+{
+    static_assert(ES::kPasses == 1, "a wave's results fit its part of the stages");
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+    asm volatile("" ::: "memory");
+    const __amdgpu_buffer_rsrc_t rc =
+        __builtin_amdgcn_make_buffer_rsrc(C, 0, (min(kRows, left) - 1) * pitch + bytes, kRawBufferWord3);
+    const int c = lane % ES::kNC, rr = lane / ES::kNC, voff = rr * pitch + 16 * c;
+#pragma unroll 4
+    for (int s = 0; s < kRows / ES::kRowsPerStore; ++s) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(ep + ES::addr(s * ES::kRowsPerStore + rr, c));
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4v{v.x, v.y, v.z, v.w}, rc, voff, s * ES::kRowsPerStore * pitch,
+                                               kBufferNt);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // One kTM x 256 tile of C (bf16) on eight waves, the ping-pong schedule of
 // gemm_bs_pp_kernel for ragged operands: A and B rows past the tile's own are
@@ -366,10 +386,8 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
     asm volatile("" ::: "memory");
 
     // epilogue: each wave stages its 64 x kWC results in a part of the stages of
-    // its own and stores whole row pieces (rows past the tile's own lie outside
-    // the buffer and are dropped)
+    // its own and stores whole row pieces
     typedef EpiStage<P::kWC, 2, 64, P::kWC * kBK> ES;
-    static_assert(ES::kPasses == 1, "a wave's results fit its part of the stages");
     const int wrow = wm * 64, wcol = wn * P::kWC;
     if (wrow >= c_rows || wcol >= c_cols) return;
     uint8_t *ep = (w < 4 ? st0 : st1) + (w & 3) * (P::kWC * kBK);
@@ -380,18 +398,7 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
 #pragma unroll
         for (int j = 0; j < 2 * kJT; ++j)
             ES::put(ep, 16 * i + fr, 4 * j + fg, pack_out4<kOutBF16, false, false>(0, acc[i][j], m, none, 0.0f));
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-    asm volatile("" ::: "memory");
-    const int pitch = (int)ldc * 2, left = min(64, c_rows - wrow);
-    const __amdgpu_buffer_rsrc_t rc = __builtin_amdgcn_make_buffer_rsrc(
-        (void *)(C + (int64_t)wrow * ldc + wcol), 0, (left - 1) * pitch + P::kWC * 2, kRawBufferWord3);
-    const int c = lane % ES::kNC, rr = lane / ES::kNC, voff = rr * pitch + 16 * c;
-#pragma unroll 4
-    for (int s = 0; s < 64 / ES::kRowsPerStore; ++s) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(ep + ES::addr(s * ES::kRowsPerStore + rr, c));
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4v{v.x, v.y, v.z, v.w}, rc, voff, s * ES::kRowsPerStore * pitch,
-                                                   kBufferNt);
-    }
+    store_rows<ES, 64>(ep, C + (int64_t)wrow * ldc + wcol, (int)ldc * 2, P::kWC * 2, c_rows - wrow, lane);
 }
 
 // fprop / dgrad in tiles of 256 rows x 256 columns; a group's last tile of at
@@ -757,8 +764,8 @@ done:
             for (int q = 0; q < 4; ++q)
                 ES::put(ep, 32 * i + tile.fr, 8 * j + 2 * q + tile.fg,
                         pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, tile.quad(i, j, q), m, none, 0.0f));
-    __syncthreads();
-    ES::store(ep, C, N, t.row0 + wm * 64, t.col0 + wn * 64, lane);
+    constexpr int kB = DC == kF32 ? 4 : 2;
+    store_rows<ES, 64>(ep, (uint8_t *)C + ((t.row0 + wm * 64) * N + t.col0 + wn * 64) * kB, N * kB, 64 * kB, 64, lane);
 }
 
 // wgrad of few tiles: a 64 x 64 tile of one group's C per block, whose four
@@ -846,8 +853,9 @@ done:
         ES::put(st1, tile.fr, 2 * q + tile.fg,
                 pack_out4<DC == kF32 ? kOutF32 : kOutBF16, false, false>(0, c, m, none, 0.0f));
     }
-    __syncthreads();
-    ES::store(st1, C, N, t.row0 + 32 * (w >> 1), t.col0 + 32 * (w & 1), lane);
+    constexpr int kB = DC == kF32 ? 4 : 2;
+    store_rows<ES, 32>(st1, (uint8_t *)C + ((t.row0 + 32 * (w >> 1)) * N + t.col0 + 32 * (w & 1)) * kB, N * kB, 32 * kB,
+                       32, lane);
 }
 
 // The tile of an fprop / dgrad launch.  Up to 12 rows a group on average most
