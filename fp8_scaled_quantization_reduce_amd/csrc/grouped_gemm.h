@@ -407,7 +407,7 @@ __device__ __forceinline__ void pp_tile(uint8_t *st0, uint8_t *st1, float *sx, c
 // two 128 x 256 tiles each (9000 rows of three 2048 x 2048 matrices 54.6 -> 49.1 us).
 //
 // Long contractions are bound by the card's power: 16384 rows over eight
-// 14336 x 4096 matrices 0.90 ms, 2.14 PFLOP/s at 1.7 GHz.  A tile also takes 6
+// 14336 x 4096 matrices 0.89 ms, 2.16 PFLOP/s at 1.7 GHz.  A tile also takes 6
 // us beside its slices (1.9 us each with the chip full): finding its group,
 // the first loads, the stores; 24594 rows over 64 matrices of 2048 x 1408, 11
 // slices, 108 us, 1.3 PFLOP/s.
@@ -513,8 +513,8 @@ __device__ __forceinline__ void group_share(int xcd, int i, int per, int &e, int
 // wgrad with bf16 results in 256 x 256 tiles of one group's C.  Every result
 // takes a multiply and a multiply-add of scales per slice, which the wave that
 // runs its products issues too: 1.9 us a slice against 0.9 of the matrix
-// unit, and 8.5 us a tile for the rest.  24594 tokens, 64 gradients of 1408 x
-// 2048: 187 us, 0.76 PFLOP/s; eight of 4096 x 4096 over 32768 tokens 560 us,
+// unit, and 7 us a tile for the rest.  24594 tokens, 64 gradients of 1408 x
+// 2048: 180 us, 0.79 PFLOP/s (190 us with the groups in their own order); eight of 4096 x 4096 over 32768 tokens 560 us,
 // 1.97 PFLOP/s.
 template <int FA, int FB>
 __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
@@ -680,12 +680,13 @@ __device__ __forceinline__ bool wgrad_tile(const uint8_t *A, const float *sA, co
 // wave reads its share of a slice from LDS into registers at once, so the
 // stage is free for the slice after next while the products run.
 //
-// Eight 14336 x 4096 gradients over 8192 tokens, fp32: 1.16 ms, 0.83 PFLOP/s,
+// Eight 14336 x 4096 gradients over 8192 tokens, fp32: 1.15 ms, 0.84 PFLOP/s,
 // 1.9 GB written.  The chip's power bounds it: in 256 x 128 ping-pong tiles of
 // one block per CU the same work took 30% more cycles at a 25% higher clock
 // (2.91 million at 2.25 GHz, here 2.23 at 1.78).  Without the loads of the
 // slices it would take 15% less time, without the widening 11%, without the
-// scales 9%.  With 1024 tokens, where the stores count, 118 us against 146.
+// scales 9%.  Eight 4096 x 4096 over 1024 tokens, where the stores count: 113
+// us against 146.
 template <int FA, int FB, int DC>
 __global__ __launch_bounds__(256, 2) void grouped_wgrad_kernel(
     const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,
@@ -926,7 +927,7 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
 // The tiles of a wgrad launch, from the time of a round of blocks in us with s
 // slices of 128 tokens per group on average.  Measured on one to sixteen
 // gradients of 768 x 1152 to 4096 x 4096 with 1 to 128 slices: 256 x 256 (bf16
-// only) 8.5 + 1.9 s per tile and CU, 128 x 128 5 + 1.3 s per two tiles and CU
+// only) 7.5 + 1.9 s per tile and CU, 128 x 128 5 + 1.3 s per two tiles and CU
 // (0.8 s where there is one; fp32 2.0 and 1.1), split 64 x 64 5 + 0.25 s per
 // tile and CU (fp32 0.31).  The large tiles reuse most of what they read, the
 // small ones fill the chip where there are few: one 768 x 1152 gradient over
@@ -945,7 +946,7 @@ inline WgradTiles wgrad_tiles(const GroupedArgs &a)
     const double two = 5.0 + (bf16 ? 1.3 : 2.0) * s, one = 5.0 + (bf16 ? 0.8 : 1.1) * s;
     const double us_small = (double)(small / (2 * cus)) * two + (last == 0 ? 0.0 : last <= cus ? one : two);
     const double us_split = up(tiles(64), cus) * (5.0 + (bf16 ? 0.25 : 0.31) * s);
-    const double us_large = up(tiles(256), cus) * (8.5 + 1.9 * s);
+    const double us_large = up(tiles(256), cus) * (7.5 + 1.9 * s);
     if (us_split < us_small && !(bf16 && us_large < us_split)) return kWgradSplit;
     return bf16 && us_large <= us_small ? kWgradLarge : kWgradSmall;
 }
