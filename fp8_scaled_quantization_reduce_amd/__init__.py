@@ -694,19 +694,17 @@ def fp8q_layernorm_backward(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=Non
     _check(lib.fp8q_layernorm_backward(*args, _stream(stream)))
 
 
-def _tensor_list(ts):
-    """Addresses, element counts and dtype codes of a list of contiguous
-    float32 / bfloat16 tensors on the current GPU, as C arrays; None if it is
-    not one (one C call per tensor and property: the list of a model's
+_T = torch.Tensor
+_dtype_of = _T.dtype.__get__
+
+
+def _addresses(ts):
+    """Addresses of a list of contiguous tensors on the current GPU, as a C
+    array (one C call per tensor and property: the list of a model's
     gradients is long)."""
-    T = torch.Tensor
-    try:
-        d = array.array("i", [_CODES[t.dtype] for t in ts])
-        if all(map(T.is_contiguous, ts)) and (not len(ts) or set(map(T.get_device, ts)) == {_current_device()}):
-            return array.array("Q", map(T.data_ptr, ts)), array.array("q", map(T.numel, ts)), d
-    except (KeyError, TypeError, AttributeError, RuntimeError):
-        pass
-    return None
+    if not all(map(_T.is_contiguous, ts)) or (len(ts) and set(map(_T.get_device, ts)) != {_current_device()}):
+        raise _Unfit
+    return array.array("Q", list(map(_T.data_ptr, ts)))
 
 
 def _address(a):
@@ -723,9 +721,13 @@ def fp8q_grad_norm_clip(grads, max_norm, norm, coef, out=None, stream=None):
     count = len(grads)
     if out is not None and len(out) != count:
         raise ValueError("out must have %d tensors, got %d" % (count, len(out)))
-    g = _tensor_list(grads)
-    o = None if out is None else _tensor_list(out)
-    if g is None or (out is not None and (o is None or o[1:] != g[1:])):
+    try:
+        types, sizes = list(map(_dtype_of, grads)), list(map(_T.numel, grads))
+        if out is not None and (list(map(_dtype_of, out)) != types or list(map(_T.numel, out)) != sizes):
+            raise _Unfit
+        d, n = array.array("i", [_CODES[t] for t in types]), array.array("q", sizes)
+        g, o = _addresses(grads), None if out is None else _addresses(out)
+    except _UNFIT:
         # find what is wrong: types and sizes first, the device last
         for i, t in enumerate(grads):
             _need(t, "grads[%d]" % i, _HP)
@@ -735,10 +737,9 @@ def fp8q_grad_norm_clip(grads, max_norm, norm, coef, out=None, stream=None):
             _ptr(t, "grads[%d]" % i)
         for i, t in enumerate(out or ()):
             _ptr(t, "out[%d]" % i)
-        raise ValueError("grads and out must be lists of GPU tensors")
-    g, n, d = g
+        raise
     # the arrays outlive the call, which reads them before it returns
-    _check(lib.fp8q_grad_norm_clip(_address(g), None if o is None else _address(o[0]), _address(n), _address(d), count,
+    _check(lib.fp8q_grad_norm_clip(_address(g), None if o is None else _address(o), _address(n), _address(d), count,
                                    max_norm, _ptr(norm, "norm"), _ptr(coef, "coef"), _stream(stream)))
 
 

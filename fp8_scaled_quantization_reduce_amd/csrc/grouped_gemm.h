@@ -931,8 +931,8 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
 // (0.8 s where there is one; fp32 2.0 and 1.1), split 64 x 64 5 + 0.25 s per
 // tile and CU (fp32 0.31).  The large tiles reuse most of what they read, the
 // small ones fill the chip where there are few: one 768 x 1152 gradient over
-// 16384 tokens 184, 93 and 36 us (bf16), eight 4096 x 4096 over 32768 548, 711
-// and more.
+// 16384 tokens 184, 93 and 36 us (bf16), eight 4096 x 4096 over 32768 548 and
+// 711 us in the large and the small ones.
 enum WgradTiles { kWgradSplit, kWgradSmall, kWgradLarge };
 
 inline WgradTiles wgrad_tiles(const GroupedArgs &a)
