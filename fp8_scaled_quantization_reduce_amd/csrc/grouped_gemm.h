@@ -862,7 +862,11 @@ done:
 // The tile of an fprop / dgrad launch.  Up to 12 rows a group on average most
 // groups fit a 16-row tile, so the weights are read once, and 32 columns a block are
 // faster than 16 unless the blocks then do not fill the chip (8 rows over
-// eight 14336 x 4096 matrices: 53.6 and 59.1 us; 64 columns 56.8 us).  Above,
+// eight 14336 x 4096 matrices: 53.6 and 59.1 us; 64 columns 56.8 us).  Up to 18
+// rows the weights still count most and 32 x 64 tiles read them faster than the
+// large ones, if they fill the chip (14 rows a group: eight 14336 x 4096 93 and
+// 102 us, 20 of 4096 x 2048 36 and 45, 64 of 2048 x 1408 39.6 and 40.6; 20 rows
+// 107 and 102, 39 and 45, 43 and 41).  Above,
 // a launch takes about `step` per round of one block per CU, `least` at the
 // least: both measured at K = 4096, one 4096-column matrix with 16 to 1024
 // rows, in us.  The steps grow slower than the tiles' areas, so the large
@@ -877,6 +881,7 @@ inline RowsTile rows_tile(const GroupedArgs &a)
     auto blocks = [&](int tm, int tn) { return max_tiles(a.rows, a.groups, tm) * ((a.N + tn - 1) / tn); };
     const int64_t live = a.rows < a.groups ? a.rows : a.groups;
     if (a.rows <= 12 * live) return blocks(16, 32) >= cus ? kRows16x32 : kRows16x16;
+    if (a.rows <= 18 * live && blocks(32, 64) >= cus) return kRows32x64;
     static const struct {
         int tm, tn;
         double least, step;
