@@ -546,20 +546,22 @@ __global__ __launch_bounds__(kBSThreads, 1) void grouped_wgrad_pp_kernel(
     pp_tile<FA, FB, kTM, true>(st0, st1, sx, a, b, kbn, 0, c, N, a_rows, b_rows);
 }
 
-// A wave's 64 x 64 tile of a wgrad.  fp32 results (kWide): the codes are
+// A wave's 64 x 64 tile, its codes read from LDS a slice at a time.  kRowB: B
+// has a scale per row (wgrad), else one for all.  fp32 results (kWide): the codes are
 // widened to bf16 (exact) and multiplied by the bf16 matrix instruction, whose
 // sums are binary32.  The FP8 instruction adds the products of eight
 // neighbouring bytes on about 15 bits under the largest of them (measured on
 // the MI355X with one large and one small product at a time), which leaves an
 // fp32 result 1.1e-5 off in the 2-norm where the widened one is 7e-8 off: below
 // the rounding of a bf16 result, above that of an fp32 one.
-template <int FA, int FB, bool kWide> struct WgradWave {
+template <int FA, int FB, bool kRowB, bool kWide> struct Wave64 {
     v16f acc[2][2];
     uint4 a[2][4], b[2][4]; // 32 rows x 128 K bytes each: chunks 4 fg .. 4 fg + 3 of row fr
     bf16x8 aw[kWide ? 2 : 1][8];
+    float wi[2];
     int fr, fg;
 
-    __device__ __forceinline__ explicit WgradWave(int lane) : fr(lane & 31), fg(lane >> 5)
+    __device__ __forceinline__ explicit Wave64(int lane) : fr(lane & 31), fg(lane >> 5)
     {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -596,12 +598,15 @@ template <int FA, int FB, bool kWide> struct WgradWave {
                 for (int s = 0; s < 8; ++s) aw[i][s] = step<FA>(a[i], s);
         }
     }
-    // the slice's products, weighted; runs of 16 rows' scales, 64 floats apart, at ga and gb
-    __device__ __forceinline__ void products(const float *ga, const float *gb)
+    // A's scales: runs of 16 rows' 64 floats apart at ga (with B's one scale at gb)
+    __device__ __forceinline__ void weights(const float *ga, const float *gb)
     {
-        float wi[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wi[i] = ga[64 * (2 * i + (fr >> 4)) + (fr & 15)];
+        for (int i = 0; i < 2; ++i) wi[i] = ga[64 * (2 * i + (fr >> 4)) + (fr & 15)] * (kRowB ? 1.0f : gb[0]);
+    }
+    // the slice's products, weighted (B's scales per row in runs at gb)
+    __device__ __forceinline__ void products(const float *gb)
+    {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             v16f p[2];
@@ -625,7 +630,9 @@ template <int FA, int FB, bool kWide> struct WgradWave {
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const v4f sb = *reinterpret_cast<const v4f *>(gb + 64 * (2 * j + (q >> 1)) + 8 * (q & 1) + 4 * fg);
+                v4f sb{1.0f, 1.0f, 1.0f, 1.0f};
+                if constexpr (kRowB)
+                    sb = *reinterpret_cast<const v4f *>(gb + 64 * (2 * j + (q >> 1)) + 8 * (q & 1) + 4 * fg);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -727,7 +734,7 @@ __global__ __launch_bounds__(256, 2) void grouped_wgrad_kernel(
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
-    WgradWave<FA, FB, DC == kF32> tile(lane);
+    Wave64<FA, FB, true, DC == kF32> tile(lane);
     load_scales(sx0, 0);
     load(st0, 0);
     load(st1, 1);
@@ -746,7 +753,8 @@ __global__ __launch_bounds__(256, 2) void grouped_wgrad_kernel(
             barrier(); // every wave has read the stage
             if ((u & 3) == 0) load_scales(u & 4 ? sx0 : sx1, kb + u + 4);
             load(st, kb + u + 2);
-            tile.products(sg + 64 * 4 * wm, sg + 64 * (8 + 4 * wn));
+            tile.weights(sg + 64 * 4 * wm, sg);
+            tile.products(sg + 64 * (8 + 4 * wn));
         }
     }
 done:
@@ -811,7 +819,7 @@ __global__ __launch_bounds__(256, 1) void grouped_wgrad_split_kernel(
             __builtin_amdgcn_raw_ptr_buffer_load_lds(t.sb, (lds_void *)(sx + 64 * (4 + run)), 4, svoff, off, 0, 0);
         }
     };
-    WgradWave<FA, FB, DC == kF32> tile(lane);
+    Wave64<FA, FB, true, DC == kF32> tile(lane);
     load_scales(sx0, 0);
     load(st0, 0);
     load(st1, 1);
@@ -829,7 +837,8 @@ __global__ __launch_bounds__(256, 1) void grouped_wgrad_split_kernel(
             asm volatile("" ::: "memory");
             if ((u & 3) == 0) load_scales(u & 4 ? sx0 : sx1, kb + u + 4);
             load(st, kb + u + 2);
-            tile.products(sg, sg + 64 * 4);
+            tile.weights(sg, sg);
+            tile.products(sg + 64 * 4);
         }
     }
 done:
@@ -859,6 +868,140 @@ done:
                        32, lane);
 }
 
+// fprop / dgrad of few tiles: a 128 x 128 tile per block, whose two sets of four
+// waves (64 x 64 each) take half of the slices each, from stages of their own,
+// and add their sums through LDS: each set finishes half of the columns.  A
+// set's chain of loads, products and scales bounds it, 1.1 us a slice: 320 rows
+// over four 4096 x 4096 matrices 22 us.
+template <int FA, int FB>
+__global__ __launch_bounds__(512, 2) void grouped_halves_kernel(const uint8_t *__restrict__ A,
+                                                                const float *__restrict__ sA,
+                                                                const uint8_t *__restrict__ B,
+                                                                const float *__restrict__ sB,
+                                                                const int32_t *__restrict__ offsets, int groups,
+                                                                int rows, int N, int K, uint16_t *__restrict__ C)
+{
+    constexpr int kTile = 128, kOp = kTile * kBK, kSx = 9 * 64; // eight runs of A's scales and B's
+    __shared__ __attribute__((aligned(1024))) uint8_t st0s[2][2 * kOp];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1s[2][2 * kOp];
+    __shared__ __attribute__((aligned(16))) float sx0s[2][kSx];
+    __shared__ __attribute__((aligned(16))) float sx1s[2][kSx];
+    GroupTiles<kTile> tiles(offsets, groups, rows);
+    const int tiles_n = N / kTile, nk = K / kBK;
+    const int n = tiles.total * tiles_n, per = (n + kXcds - 1) / kXcds;
+    const int i = blockIdx.x / kXcds, t = (int)(blockIdx.x % kXcds) * per + i;
+    if (i >= per || t >= n) return;
+    const GroupTile gt = tiles.find(t / tiles_n);
+    int tm, tn;
+    group_tile(gt.tile * tiles_n + t % tiles_n, (gt.size + kTile - 1) / kTile, tiles_n, tm, tn);
+    const int64_t row0 = gt.row0 + kTile * tm, n0 = kTile * tn;
+    const int a_rows = min(kTile, gt.size - kTile * tm);
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+    const int h = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), wm = w & 1, wn = w >> 1;
+    // both sets run `each` slices; the second one's last may be past the end: zeros
+    const int each = (nk + 1) / 2, k0 = h * each, kn = min(each, nk - k0);
+    const __amdgpu_buffer_rsrc_t ra =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(A + row0 * K), 0, a_rows * K, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(B + ((int64_t)gt.group * N + n0) * K), 0, kTile * K, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rsa =
+        __builtin_amdgcn_make_buffer_rsrc((void *)(sA + row0 * nk), 0, a_rows * nk * 4, kRawBufferWord3);
+    const __amdgpu_buffer_rsrc_t rsb = __builtin_amdgcn_make_buffer_rsrc(
+        (void *)(sB + ((int64_t)gt.group * (N / kTile) + tn) * nk), 0, nk * 4, kRawBufferWord3);
+    const int voff = (lane >> 3) * K + (((lane & 7) ^ ((4 * w + (lane >> 4)) & 7)) << 4);
+    const int svoff = ((lane & 15) * nk + (lane >> 4)) * 4;
+    uint8_t *st0 = st0s[h], *st1 = st1s[h];
+    float *sx0 = sx0s[h], *sx1 = sx1s[h];
+    auto load = [&](uint8_t *st, int k) {
+        const int at = k < kn ? (k0 + k) * kBK : 1 << 30;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int row = 8 * (w + 4 * u), off = row * K + at;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(st + row * kBK), 16, voff, off, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(st + kOp + row * kBK), 16, voff, off, 0, 0);
+        }
+    };
+    // scales of slices k .. k + 3, runs of 16 rows as [slice][row]; every wave loads B's
+    auto load_scales = [&](float *sx, int k) {
+        const int at = k0 + k < nk ? (k0 + k) * 4 : 1 << 30;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int run = w + 4 * u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(sx + 64 * run), 4, svoff, 16 * run * nk * 4 + at,
+                                                     0, 0);
+        }
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(sx + 64 * 8), 4, (lane >> 4) * 4, at, 0, 0);
+    };
+    auto barrier = [&]() {
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    Wave64<FA, FB, false, false> tile(lane);
+    float wq[4][2];
+    load_scales(sx0, 0);
+    load(st0, 0);
+    load(st1, 1);
+    for (int kb = 0;; kb += 8) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (kb + u >= each) goto done;
+            uint8_t *st = u & 1 ? st1 : st0;
+            const float *sg = u & 4 ? sx1 : sx0;
+            if ((u & 3) == 1) __builtin_amdgcn_s_waitcnt(waitcnt_imm(11, 15));
+            else __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 15));
+            barrier();
+            tile.read(st + wm * 64 * kBK, st + kOp + wn * 64 * kBK);
+            // four slices' scales at once: the compiler waits for every load in
+            // flight before it reads them
+            if ((u & 3) == 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    tile.weights(sg + 16 * k + 64 * 4 * wm, sg + 16 * k + 64 * 8);
+                    wq[k][0] = tile.wi[0], wq[k][1] = tile.wi[1];
+                }
+            }
+            tile.wi[0] = wq[u & 3][0], tile.wi[1] = wq[u & 3][1];
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            barrier(); // every wave has read the stage
+            if ((u & 3) == 0) load_scales(u & 4 ? sx0 : sx1, kb + u + 4);
+            load(st, kb + u + 2);
+            tile.products(nullptr);
+        }
+    }
+done:
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __syncthreads();
+    // the other set's columns go to it, 32 of the wave's 64
+    v4f(*mine)[64] = reinterpret_cast<v4f(*)[64]>(st0 + w * 8192);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (j != h) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mine[4 * i + q][lane] = tile.quad(i, j, q);
+        }
+    __syncthreads();
+    const v4f(*other)[64] = reinterpret_cast<const v4f(*)[64]>(st0s[1 - h] + w * 8192);
+    typedef EpiStage<32, 2, 64, 4096> ES;
+    uint8_t *ep = st1 + w * 4096;
+    uint32_t m = 0;
+    const Epi none{nullptr, kActNone, nullptr};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (j == h) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    ES::put(ep, 32 * i + tile.fr, 2 * q + tile.fg,
+                            pack_out4<kOutBF16, false, false>(0, tile.quad(i, j, q) + other[4 * i + q][lane], m, none,
+                                                              0.0f));
+        }
+    if (64 * wm < a_rows)
+        store_rows<ES, 64>(ep, C + (row0 + 64 * wm) * N + n0 + 64 * wn + 32 * h, N * 2, 64, a_rows - 64 * wm, lane);
+}
+
 // The tile of an fprop / dgrad launch.  Up to 12 rows a group on average most
 // groups fit a 16-row tile, so the weights are read once, and 32 columns a block are
 // faster than 16 unless the blocks then do not fill the chip (8 rows over
@@ -872,8 +1015,9 @@ done:
 // rows, in us.  The steps grow slower than the tiles' areas, so the large
 // ping-pong tiles win as soon as they fill a part of the chip: 256 rows over
 // those eight matrices 109 us against 132 us in 32 x 64 tiles, but 40 rows of
-// one 4096 x 4096 matrix 11.7 us in 32 x 32 tiles against 29 us.
-enum RowsTile { kRows16x16, kRows16x32, kRows32x32, kRows32x64, kRows64x64, kRowsPP };
+// one 4096 x 4096 matrix 11.7 us in 32 x 32 tiles against 29 us, and in between
+// 320 rows over four 22 us in 128 x 128 tiles against 30 in the large ones.
+enum RowsTile { kRows16x16, kRows16x32, kRows32x32, kRows32x64, kRowsHalves, kRowsPP };
 
 inline RowsTile rows_tile(const GroupedArgs &a)
 {
@@ -885,8 +1029,8 @@ inline RowsTile rows_tile(const GroupedArgs &a)
     static const struct {
         int tm, tn;
         double least, step;
-    } cost[6] = {{16, 16, 8.7, 5.0},   {16, 32, 8.8, 7.2},   {32, 32, 11.5, 10.5},
-                 {32, 64, 15.4, 14.5}, {64, 64, 22.5, 22.0}, {256, 256, 40.0, 40.0}};
+    } cost[6] = {{16, 16, 8.7, 5.0},   {16, 32, 8.8, 7.2},     {32, 32, 11.5, 10.5},
+                 {32, 64, 15.4, 14.5}, {128, 128, 21.0, 21.0}, {256, 256, 40.0, 40.0}};
     RowsTile best = kRowsPP;
     double least = 0.0;
     for (int i = kRowsPP; i >= kRows16x16; --i) {
@@ -917,7 +1061,12 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
         break;
     case kRows32x32: FP8Q_ROWS(2, 2, 8); break;
     case kRows32x64: FP8Q_ROWS(2, 4, 4); break;
-    case kRows64x64: FP8Q_ROWS(4, 4, 4); break;
+    case kRowsHalves: {
+        const int64_t tiles = max_tiles(a.rows, a.groups, 128) * (a.N / 128);
+        grouped_halves_kernel<FA, FB><<<(unsigned)(tiles + kXcds), 512, 0, a.stream>>>(
+            a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C);
+        break;
+    }
     default: {
         const int64_t tiles = max_tiles(a.rows, a.groups, 256) * ((a.N + 255) / 256);
         const int cus = a.cus / kXcds > 1 ? a.cus / kXcds : 1; // of an XCD

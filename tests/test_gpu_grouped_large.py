@@ -235,3 +235,10 @@ def test_gemm_few_rows_over_long_contractions(k):
     """Fewer, as many and more slices than the waves that share a tile's contraction."""
     sizes = [1, 0, 9, 16, 17, 3] * 4
     check_rows(sizes, 2048, k, np.arange(sum(sizes)), np.arange(0, 2048, 3))
+
+
+@pytest.mark.parametrize("k", [128, 256, 640, 1152, 2048, 2176])
+@pytest.mark.parametrize("sizes,n", [([130, 0, 61, 128, 257, 100], 1024), ([900, 1100], 512), ([90, 120, 70], 4096)])
+def test_gemm_of_few_tiles(sizes, n, k):
+    """Few tiles whose slices two halves of a block share: one, odd and even numbers of slices."""
+    check_rows(sizes, n, k, np.arange(sum(sizes)), np.arange(0, n, 5), fa=E5 if k % 512 else E4)
