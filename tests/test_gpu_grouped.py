@@ -211,7 +211,7 @@ def test_gemm_other_formats(fa, fb):
 
 
 # one launch per tile that the rule on rows, groups and N picks (16 x 16 to
-# 64 x 64 blocks, the large tiles with full, half and one-row remainders), with
+# 128 x 128 blocks, the large tiles with full, half and one-row remainders), with
 # one, few, odd and even numbers of slices
 TILE_CASES = [([9, 0, 3], 128, 384), ([8] * 40, 256, 128), ([33, 7], 4096, 128), ([128], 4096, 256),
               ([100, 141], 4096, 384), ([700, 130, 0, 1000, 170], 1152, 128), ([257, 1, 900, 384, 129], 1152, 384),
