@@ -899,6 +899,7 @@ __global__ __launch_bounds__(512, 2) void grouped_halves_kernel(const uint8_t *_
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
     const int h = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), wm = w & 1, wn = w >> 1;
     // both sets run `each` slices; the second one's last may be past the end: zeros
+    // for its codes and for its scales
     const int each = (nk + 1) / 2, k0 = h * each, kn = min(each, nk - k0);
     const __amdgpu_buffer_rsrc_t ra =
         __builtin_amdgcn_make_buffer_rsrc((void *)(A + row0 * K), 0, a_rows * K, kRawBufferWord3);
@@ -921,14 +922,17 @@ __global__ __launch_bounds__(512, 2) void grouped_halves_kernel(const uint8_t *_
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(st + kOp + row * kBK), 16, voff, off, 0, 0);
         }
     };
-    // scales of slices k .. k + 3, runs of 16 rows as [slice][row]; every wave loads B's
+    // Scales of slices k .. k + 3, runs of 16 rows as [slice][row]; every wave loads
+    // B's.  A lane whose slice is past a row's last reads a zero: the next row's
+    // first scale may be infinite or NaN, which the slice's zeros would not cancel.
     auto load_scales = [&](float *sx, int k) {
-        const int at = k0 + k < nk ? (k0 + k) * 4 : 1 << 30;
+        const int at = (k0 + k) * 4;
+        const int sav = k0 + k + (lane >> 4) < nk ? svoff : kTile * nk * 4; // the latter outside the buffer
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int run = w + 4 * u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(sx + 64 * run), 4, svoff, 16 * run * nk * 4 + at,
-                                                     0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(sx + 64 * run), 4, sav, 16 * run * nk * 4 + at, 0,
+                                                     0);
         }
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(sx + 64 * 8), 4, (lane >> 4) * 4, at, 0, 0);
     };
