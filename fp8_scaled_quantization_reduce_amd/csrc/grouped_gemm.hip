@@ -28,6 +28,10 @@ hipError_t launch_grouped_wgrad(const uint8_t *A, int fa, const float *sA, const
                                 int64_t N, void *C, int c_dtype, hipStream_t s)
 {
     if (groups == 0 || M == 0 || N == 0) return hipSuccess;
+    // Rows from `stride` on cannot be in the columnwise copies.  Without them the
+    // blocks of up to 2^16 groups of any offsets add up to at most 2^30, which the
+    // kernels' 32-bit sums hold.
+    if (rows > stride) rows = stride;
     const GroupedArgs a{A, B, sA, sB, offsets, groups, (int)rows, M, N, 0, stride, C, c_dtype, s, compute_units()};
     if (fa == kE4M3) return fb == kE4M3 ? launch_grouped_wgrad_e4m3_e4m3(a) : launch_grouped_wgrad_e4m3_e5m2(a);
     return fb == kE4M3 ? launch_grouped_wgrad_e5m2_e4m3(a) : launch_grouped_wgrad_e5m2_e5m2(a);

@@ -5,8 +5,11 @@
 // `rows` rows.  The offsets are device data that the host never sees, so a
 // launch covers the most tiles that any offsets could need (max_tiles) and
 // each block looks its tile up: a wave reads 64 groups at a time, counts
-// their tiles and scans the counts (GroupTiles).  Offsets are clamped to 0 .. rows and to
-// not decrease, so whatever they hold, every tile lies inside the buffer.
+// their tiles and scans the counts (GroupTiles).  Offsets are clamped to 0 .. rows
+// and a group that would end before it starts is empty, so whatever they hold,
+// every tile lies inside the buffer.  Groups of offsets that decrease may share
+// rows, and their tiles then be more than a launch covers (or than 32 bits hold):
+// the count of tiles ends at what the groups of one buffer can have.
 //
 // The token-contiguous (columnwise) copies give every group whole blocks of
 // 128 columns: with tiles of 128 rows, tile t of the numbering below is
@@ -53,7 +56,7 @@ template <int kTile> struct GroupTiles {
     const int32_t *offsets;
     int groups, rows;
     int lo, size, count, sum; // of group 64 i + lane, for the chunk held
-    int total;                // tiles of all groups
+    int total;                // tiles of all groups, at most rows / kTile + groups
 
     __device__ __forceinline__ void hold(int g0)
     {
@@ -65,7 +68,7 @@ template <int kTile> struct GroupTiles {
     {
         for (int g0 = 0; g0 < groups; g0 += 64) {
             hold(g0);
-            total += __builtin_amdgcn_readlane(sum, 63);
+            total = min(total + __builtin_amdgcn_readlane(sum, 63), rows / kTile + groups);
         }
     }
     // the group that holds tile t, 0 <= t < total

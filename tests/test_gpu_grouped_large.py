@@ -242,3 +242,27 @@ def test_gemm_few_rows_over_long_contractions(k):
 def test_gemm_of_few_tiles(sizes, n, k):
     """Few tiles whose slices two halves of a block share: one, odd and even numbers of slices."""
     check_rows(sizes, n, k, np.arange(sum(sizes)), np.arange(0, n, 5), fa=E5 if k % 512 else E4)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wgrad_of_offsets_whose_blocks_pass_32_bits(dtype):
+    """Offsets that fall back to 0 after every group, over many more rows than
+    the copies have columns: the blocks before a group number up to 2^32.  The
+    first group's block is in the copies, all others lie past them."""
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    groups, rows = 65536, 1 << 24
+    a, sa, b, sb = codes(gen, 128, 128), scales(gen, 128, 1), codes(gen, 128, 128), scales(gen, 128, 1)
+    off = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = rows
+    buf = torch.full((groups * 128 * 128 + 256,), 7.0, dtype=dtype, device="cuda")
+    c = buf[128:-128].view(groups, 128, 128)
+    status = fq.lib.fp8_grouped_gemm_wgrad(a.data_ptr(), E5, sa.data_ptr(), b.data_ptr(), E4, sb.data_ptr(),
+                                           off.data_ptr(), groups, rows, 128, 128, 128, c.data_ptr(),
+                                           fq.F32 if dtype == torch.float32 else fq.BF16,
+                                           torch.cuda.current_stream().cuda_stream)
+    assert status == fq.OK, fq.last_error()
+    wa = value(a, E5) * np.repeat(host(sa).astype(np.float64), 128, 1)
+    wb = value(b, E4) * np.repeat(host(sb).astype(np.float64), 128, 1)
+    close(c[0], wa, wb, 128, dtype == torch.bfloat16)
+    assert not c[1:].any()
+    assert torch.all(buf[:128] == 7.0) and torch.all(buf[-128:] == 7.0)
