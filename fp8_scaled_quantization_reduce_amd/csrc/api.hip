@@ -1131,15 +1131,17 @@ static int fp8_quantize_grouped_impl(const void *x, int32_t dtype, int64_t x_row
     if (cols % 128) return fail(FP8Q_EUNSUPPORTED, "%s: cols must be a multiple of 128", fn);
     if (x_rows > (int64_t)1 << 31 || cols > (int64_t)1 << 24)
         return fail(FP8Q_EUNSUPPORTED, "%s: x_rows exceeds 2^31 or cols 2^24", fn);
-    if (!row_index && rows != x_rows) return fail(FP8Q_EINVAL, "%s: rows must equal x_rows without a row_index", fn);
     if (row_index && !aligned(row_index, 4)) return fail(FP8Q_EINVAL, "%s: row_index must be 4-byte aligned", fn);
-    if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr))
-        return fail(FP8Q_EINVAL, "%s: codes and scales of a copy go together", fn);
-    if (!q_row && !q_col) return fail(FP8Q_EINVAL, "%s: at least one of q_row / q_col is needed", fn);
     if (q_col && (col_stride < 0 || col_stride % 128))
         return fail(FP8Q_EINVAL, "%s: col_stride must be a multiple of 128", fn);
     if (!q_col) col_stride = 0;
+    // without rows the buffers are empty and may be null
     if (rows > 0 && cols > 0) {
+        if (!row_index && rows != x_rows)
+            return fail(FP8Q_EINVAL, "%s: rows must equal x_rows without a row_index", fn);
+        if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr))
+            return fail(FP8Q_EINVAL, "%s: codes and scales of a copy go together", fn);
+        if (!q_row && !q_col) return fail(FP8Q_EINVAL, "%s: at least one of q_row / q_col is needed", fn);
         if ((x_rows > 0 && !x) || !aligned(x, 16)) return fail(FP8Q_EINVAL, "%s: x must be a 16-byte aligned pointer", fn);
         if (!aligned(q_row, 16) || !aligned(q_col, 16) || !aligned(s_row, 4) || !aligned(s_col, 4))
             return fail(FP8Q_EINVAL, "%s: codes must be 16-byte and scales 4-byte aligned", fn);

@@ -460,7 +460,9 @@ int fp8_quantize_error_feedback(const void *g, int32_t dtype, float *residual, i
  *           rows + 127 * min(groups, rows), rounded up to a block); columns past
  *           it are not written, and groups that do not fit it are left out
  *           of the columnwise copy.
- *   Each copy is nullable (codes and scales together), not both.
+ *   Each copy is nullable (codes and scales together), not both.  With no
+ *   rows (no token came to these groups) the call does nothing, and x,
+ *   row_index and the copies, which are empty, may be null.
  * Errors: FP8Q_EINVAL for unknown enums, a copy without its scales, no copy,
  * misalignment, overlapping buffers; FP8Q_EUNSUPPORTED for cols not a
  * multiple of 128, more than 65536 groups or 2^31 rows.

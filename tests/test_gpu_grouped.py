@@ -422,3 +422,21 @@ def test_streams_and_graph_replay():
         assert torch.equal(outs[0]["qr"], outs[1]["qr"])
         assert torch.equal(outs[0]["qc"][:, :used], outs[1]["qc"][:, :used])
         assert torch.equal(outs[0]["c"], outs[1]["c"]) and torch.equal(outs[0]["w"], outs[1]["w"])
+
+
+def test_quantize_no_rows():
+    """No token for any expert of this rank: every buffer is empty."""
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    e = lambda *s: torch.empty(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    f = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    for x, index in ((torch.empty(0, 256, device="cuda"), None),
+                     (torch.ones(9, 256, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"))):
+        fq.fp8_quantize_grouped(x, off, E4, row_index=index, q_row=e(0, 256), s_row=f(0, 2))
+        fq.fp8_quantize_grouped(x, off, E4, row_index=index, q_row=e(0, 256), s_row=f(0, 2), q_col=e(256, 0),
+                                s_col=f(256, 0))
+        qc, sc = empty_codes((256, 384)), empty_f32((256, 3))
+        fq.fp8_quantize_grouped(x, off, E4, row_index=index, q_col=qc, s_col=sc)
+        assert torch.all(qc == 0xA5) and torch.all(sc == -7.25)
+    dw = torch.full((3, 256, 128), 5.0, device="cuda")
+    fq.fp8_grouped_gemm_wgrad(e(256, 0), E5, f(256, 0), e(128, 0), E4, f(128, 0), off, dw)
+    assert not dw.any()

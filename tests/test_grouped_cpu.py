@@ -134,3 +134,16 @@ def test_binding_refuses(i):
     call, exc, fragment = BAD_CALLS[i]
     with pytest.raises(exc, match=fragment):
         call()
+
+
+def test_quantize_grouped_without_rows_does_nothing():
+    """An expert rank that got no tokens: the buffers are empty, so their
+    addresses are null."""
+    for index, x_rows, qc in ((None, 0, None), (None, 64, None), (P[1], 64, None), (None, 64, P[5])):
+        assert _q(x=P[0] if x_rows else None, x_rows=x_rows, index=index, rows=0, qr=None, sr=None, qc=qc,
+                  sc=P[6] if qc else None) == fq.OK, fq.last_error()
+    assert _q(cols=0, qr=None, sr=None, qc=None, sc=None) == fq.OK, fq.last_error()
+    # what is wrong without rows too is still refused
+    _expect(_q(rows=0, dt=2), fq.EINVAL, "dtype")
+    _expect(_q(rows=0, off=None), fq.EINVAL, "offsets")
+    _expect(_q(rows=0, stride=500), fq.EINVAL, "col_stride")
