@@ -3,7 +3,7 @@
 //   norm = sqrt(sum over all tensors and elements of g^2)
 //   coef = min(1, max_norm / (norm + 1e-6)),  out = g coef
 // A NaN anywhere gives a NaN norm and a NaN coefficient; an infinite gradient
-// gives an infinite norm and the coefficient 0.
+// gives an infinite norm and the coefficient 0 (1 where max_norm is infinite).
 //
 // The tensors of a launch are a table in the kernel's arguments, so a call
 // copies nothing to the device.  Each tensor is cut into units of kUnit
@@ -155,6 +155,7 @@ __device__ __forceinline__ float clip_coef(const double *sq, int parts, float ma
         if (i < parts) s += sq[i];
     }
     norm = (float)sqrt(block_sum(s));
+    if (max_norm == __builtin_inff()) return norm == norm ? 1.0f : norm; // no bound: inf / inf is not asked
     const float c = max_norm / (norm + 1e-6f);
     return c > 1.0f ? 1.0f : c; // a NaN stays
 }

@@ -557,14 +557,14 @@ int fp8q_layernorm_backward_workspace(int32_t dtype, int64_t rows, int64_t cols,
  *   coef = min(1, max_norm / (norm + 1e-6)),  out = g coef.
  * The squares are summed in binary64 in a fixed order; norm and coef are
  * binary32, each out element is rounded once to its type.  A NaN gradient
- * gives a NaN norm and coefficient (and so NaN gradients), an infinite one an
- * infinite norm and the coefficient 0.
+ * gives a NaN norm and coefficient (and so NaN gradients), an infinite one, or
+ * a norm past binary32, an infinite norm and the coefficient 0.
  *   g      HOST array of `count` device pointers; tensor i has n[i] >= 0
  *          elements of dtype[i] (host arrays too), aligned to its elements
  *   out    HOST array of device pointers of the same sizes and types, each
  *          equal to g[i] or overlapping no gradient; NULL: in place
- *   max_norm  not negative; +inf: only norm (and coef = 1) are computed, and
- *          out must be NULL
+ *   max_norm  not negative; +inf: only the norm is computed, coef is 1 (also
+ *          with an infinite norm; NaN with a NaN norm) and out must be NULL
  *   norm, coef  one device float each
  * The arrays are read before the call returns.  The call enqueues two
  * launches for up to 128 tensors (and two more for every further 128).  Its

@@ -153,3 +153,14 @@ def test_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(got[0], norm) and torch.equal(got[1], coef)
         assert all(torch.equal(a, b) for a, b in zip(got[2], out))
+
+
+def test_norm_alone_of_nonfinite_gradients():
+    """Without a bound nothing is clipped, by an infinite norm neither; a NaN shows in both results."""
+    big = [torch.full((5,), 3e38), torch.full((9000,), 3e38)]  # a norm past binary32
+    for grads, nan in (([torch.tensor([1.0, math.inf, 2.0])], False), (big, False),
+                       ([torch.tensor([1.0, math.nan]), torch.ones(3, dtype=torch.bfloat16)], True),
+                       ([torch.tensor([math.inf, math.nan])], True)):
+        norm, coef, out = run(grads, math.inf, "in place")
+        assert math.isnan(norm) and math.isnan(coef) if nan else norm == math.inf and coef == 1.0
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, grads))
