@@ -437,17 +437,19 @@ __global__ __launch_bounds__(kLnLong) void ln_bwd_long(const typename Elem<DT>::
     }
 }
 
-// Sums of dy xh and dy of 64 columns over a share of the rows (long rows):
-// four waves take rows in turn, then fold through LDS into slot blockIdx.y.
+// Sums of dy xh and dy of 64 columns (the launch's from c0 on) over a share of
+// the rows (long rows): four waves take rows in turn, then fold through LDS
+// into slot blockIdx.y.
 template <int DT>
 __global__ __launch_bounds__(kLnThreads) void ln_bwd_cols(const typename Elem<DT>::type *__restrict__ dy,
                                                           const typename Elem<DT>::type *__restrict__ x, int64_t rows,
                                                           int64_t cols, const float *__restrict__ mean,
-                                                          const float *__restrict__ rstd, float *__restrict__ ws)
+                                                          const float *__restrict__ rstd, float *__restrict__ ws,
+                                                          int64_t c0)
 {
     __shared__ float lds[2][4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    const int64_t c = c0 + (int64_t)blockIdx.x * 64 + lane;
     float dg = 0.0f, db = 0.0f;
     if (c < cols) {
         for (int64_t row = (int64_t)blockIdx.y * 4 + wave; row < rows; row += (int64_t)gridDim.y * 4) {
@@ -464,19 +466,19 @@ __global__ __launch_bounds__(kLnThreads) void ln_bwd_cols(const typename Elem<DT
             lds[wave][0][lane] + lds[wave][1][lane] + lds[wave][2][lane] + lds[wave][3][lane];
 }
 
-// Fold `slots` partial rows of the workspace: 32 columns per block, 32 lanes
-// per column taking slots in turn, eight loads in flight each.  blockIdx.y: 0
-// dgamma, 1 dbeta.  The memory's latency bounds it: 799 slots of 147 columns
+// Fold `slots` partial rows of the workspace: 32 columns per block (the launch's
+// from c0 on), 32 lanes per column taking slots in turn, eight loads in flight
+// each.  blockIdx.y: 0 dgamma, 1 dbeta.  The memory's latency bounds it: 799 slots of 147 columns
 // 26 us with eight lanes and a load at a time, 4.5 us so.
 template <int PT>
 __global__ __launch_bounds__(kFoldThreads) void ln_bwd_fold(const float *__restrict__ ws, int slots, int64_t cols,
                                                             typename Elem<PT>::type *__restrict__ dgamma,
-                                                            typename Elem<PT>::type *__restrict__ dbeta)
+                                                            typename Elem<PT>::type *__restrict__ dbeta, int64_t c0)
 {
     constexpr int kLanes = kFoldThreads / 32;
     __shared__ float lds[kLanes][32];
     const int j = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + j;
+    const int64_t c = c0 + (int64_t)blockIdx.x * 32 + j;
     typename Elem<PT>::type *out = blockIdx.y ? dbeta : dgamma;
     if (!out) return;
     float s = 0.0f;
@@ -538,6 +540,9 @@ LnShape bwd_shape(int64_t cols, int vec)
 #define FP8Q_LN_BWD_SHAPES_BF16(X) X(512, 4)
 int vec_of(int dtype) { return dtype == kF32 ? 4 : 8; }
 
+// Most blocks of a launch: one of 2^32 lanes or more is cut off without an
+// error.  Rows beyond are walked, columns (ln_bwd_cols, ln_bwd_fold) get a
+// launch more; walking them too cost ln_bwd_cols 2%.
 constexpr int64_t kLnMaxGrid = 1 << 20;
 // Blocks of the backward pass, each of which leaves one partial row: two per
 // CU where a block shares a row, four where its waves have rows of their own
@@ -612,6 +617,13 @@ hipError_t bwd(const void *dy_, const void *x_, int64_t rows, int64_t cols, cons
     const bool params = dgamma || dbeta;
     const LnShape sh = bwd_shape(cols, Elem<DT>::kVec);
     const int slots = bwd_slots(rows, cols, DT);
+    // launches of blocks of `width` columns each
+    auto by_columns = [&](int width, auto launch) {
+        for (int64_t c0 = 0; c0 < cols; c0 += kLnMaxGrid * width) {
+            const int64_t blocks = (cols - c0 + width - 1) / width;
+            launch((unsigned)(blocks < kLnMaxGrid ? blocks : kLnMaxGrid), c0);
+        }
+    };
     if (rows > 0) {
         const int grid = sh.lanes ? bwd_blocks(rows, sh) : (int)(rows < kLnMaxGrid ? rows : kLnMaxGrid);
         float *w = params ? ws : nullptr;
@@ -631,14 +643,18 @@ hipError_t bwd(const void *dy_, const void *x_, int64_t rows, int64_t cols, cons
         if (sh.lanes == 0) {
             ln_bwd_long<DT, PT><<<grid, kLnLong, 0, s>>>(dy, x, rows, cols, gamma, mean, rstd, dx);
             if (params)
-                ln_bwd_cols<DT><<<dim3((unsigned)((cols + 63) / 64), (unsigned)slots), kLnThreads, 0, s>>>(
-                    dy, x, rows, cols, mean, rstd, w);
+                by_columns(64, [&](unsigned blocks, int64_t c0) {
+                    ln_bwd_cols<DT><<<dim3(blocks, (unsigned)slots), kLnThreads, 0, s>>>(dy, x, rows, cols, mean, rstd,
+                                                                                        w, c0);
+                });
         }
     }
     // no rows: the parameter gradients are zero
     if (params)
-        ln_bwd_fold<PT><<<dim3((unsigned)((cols + 31) / 32), 2), kFoldThreads, 0, s>>>(ws, rows > 0 ? slots : 0, cols,
-                                                                                       (P *)dgamma, (P *)dbeta);
+        by_columns(32, [&](unsigned blocks, int64_t c0) {
+            ln_bwd_fold<PT><<<dim3(blocks, 2), kFoldThreads, 0, s>>>(ws, rows > 0 ? slots : 0, cols, (P *)dgamma,
+                                                                     (P *)dbeta, c0);
+        });
     return hipGetLastError();
 }
 

@@ -226,3 +226,21 @@ def test_on_another_stream():
     fq.fp8q_layernorm(xd, g, b, 1e-5, y, stream=s)
     s.synchronize()
     assert torch.equal(y.cpu(), want)
+
+
+def test_backward_of_more_columns_than_one_launch_of_the_fold_has_lanes():
+    """2^27 columns and a few: with one row, dgamma = dy xh and dbeta = dy."""
+    cols = (1 << 27) + 77
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, cols, generator=gen, device="cuda").to(torch.bfloat16)
+    dy = torch.randn(1, cols, generator=gen, device="cuda").to(torch.bfloat16)
+    mean, rstd = torch.full((1,), 0.25, device="cuda"), torch.full((1,), 1.5, device="cuda")
+    dx = torch.empty_like(x)
+    dg, db = (torch.full((cols + 64,), 777.0, device="cuda") for _ in range(2))
+    ws = torch.empty(fq.fp8q_layernorm_backward_workspace(fq.BF16, 1, cols), dtype=torch.uint8, device="cuda")
+    fq.fp8q_layernorm_backward(dy, x, None, mean, rstd, dx, dg[:cols], db[:cols], ws)
+    assert torch.equal(db[:cols], dy[0].float())
+    want = dy[0].double() * ((x[0].double() - 0.25) * 1.5)
+    # x - mean, its product with rstd (exact here but for one rounding each) and with dy
+    assert torch.all((dg[:cols].double() - want).abs() <= 4 * U * want.abs())
+    assert torch.all(dg[cols:] == 777.0) and torch.all(db[cols:] == 777.0)
