@@ -52,6 +52,10 @@ constexpr uint32_t kPollRounds = 1u << 21;
 #endif
 constexpr int kMaxGrid = FP8Q_MAX_GRID;
 
+// Most blocks of `lanes` lanes in one direction of a launch: from 2^32 lanes on
+// the runtime cuts a launch off without an error (found on the MI355X).
+constexpr int64_t max_blocks(int lanes) { return 0xFFFFFFFFll / lanes; }
+
 // Scratch slots per device: one per stream that has run a reducing call.
 constexpr int kScratchSlots = 64;
 

@@ -174,7 +174,7 @@ template <int F, int DT>
 __global__ __launch_bounds__(kGqThreads, 4) void tile_both_kernel(
     const typename In<DT>::type *__restrict__ x, int64_t x_rows, int64_t cols, const int32_t *__restrict__ index,
     int rows, const int32_t *__restrict__ offsets, int groups, uint8_t *__restrict__ q_row, float *__restrict__ s_row,
-    uint8_t *__restrict__ q_col, float *__restrict__ s_col, int64_t stride)
+    uint8_t *__restrict__ q_col, float *__restrict__ s_col, int64_t stride, int t0)
 {
     constexpr int kDw = Piece<DT>::kDw, kPer = 16 / kDw; // elements per dword
     __shared__ __attribute__((aligned(16))) uint32_t tl[128 * 32]; // column codes, [column][row / 4]
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(kGqThreads, 4) void tile_both_kernel(
     __shared__ float colscale[128];
     __shared__ uint32_t colbad; // some column scale is NaN, infinite or zero
     const int blocks_c = (int)(cols / 128);
-    const int t = (int)(blockIdx.x / blocks_c), cb = (int)(blockIdx.x % blocks_c);
+    const int t = t0 + (int)(blockIdx.x / blocks_c), cb = (int)(blockIdx.x % blocks_c);
     GroupTiles<128> tiles(offsets, groups, rows);
     if (t >= tiles.total) return;
     const GroupTile gt = tiles.find(t);
@@ -285,9 +285,14 @@ hipError_t launch(const void *x_, int64_t x_rows, int64_t cols, const int32_t *i
         auto k = four ? rows_kernel<F, DT, 4> : rows_kernel<F, DT, 1>;
         k<<<(int)(g < kMaxGrid ? g : kMaxGrid), kGqThreads, 0, s>>>(x, x_rows, cols, index, rows, q_row, s_row);
     } else {
-        const int64_t g = max_tiles(rows, groups, 128) * (cols / 128);
-        tile_both_kernel<F, DT><<<(unsigned)g, kGqThreads, 0, s>>>(x, x_rows, cols, index, (int)rows, offsets, groups,
-                                                                   q_row, s_row, q_col, s_col, stride);
+        // in launches of as many tiles as one holds
+        const int64_t tiles = max_tiles(rows, groups, 128), most = max_blocks(kGqThreads) / (cols / 128);
+        for (int64_t t0 = 0; t0 < tiles; t0 += most) {
+            const int64_t g = (tiles - t0 < most ? tiles - t0 : most) * (cols / 128);
+            tile_both_kernel<F, DT><<<(unsigned)g, kGqThreads, 0, s>>>(x, x_rows, cols, index, (int)rows, offsets,
+                                                                       groups, q_row, s_row, q_col, s_col, stride,
+                                                                       (int)t0);
+        }
     }
     return hipGetLastError();
 }

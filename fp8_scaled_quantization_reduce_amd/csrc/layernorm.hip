@@ -540,9 +540,9 @@ LnShape bwd_shape(int64_t cols, int vec)
 #define FP8Q_LN_BWD_SHAPES_BF16(X) X(512, 4)
 int vec_of(int dtype) { return dtype == kF32 ? 4 : 8; }
 
-// Most blocks of a launch: one of 2^32 lanes or more is cut off without an
-// error.  Rows beyond are walked, columns (ln_bwd_cols, ln_bwd_fold) get a
-// launch more; walking them too cost ln_bwd_cols 2%.
+// Most blocks of a launch (max_blocks ends below 2^22 of 1024 lanes).  Rows
+// beyond are walked, columns (ln_bwd_cols, ln_bwd_fold) get a launch more;
+// walking them too cost ln_bwd_cols 2%.
 constexpr int64_t kLnMaxGrid = 1 << 20;
 // Blocks of the backward pass, each of which leaves one partial row: two per
 // CU where a block shares a row, four where its waves have rows of their own

@@ -266,3 +266,29 @@ def test_wgrad_of_offsets_whose_blocks_pass_32_bits(dtype):
     close(c[0], wa, wb, 128, dtype == torch.bfloat16)
     assert not c[1:].any()
     assert torch.all(buf[:128] == 7.0) and torch.all(buf[-128:] == 7.0)
+
+
+def test_quantize_more_tiles_than_one_launch_holds():
+    """65536 groups, a few of them with rows: tiles for all that offsets could
+    ask for, more than 2^32 lanes.  Codes and scales of both copies against the same
+    rows quantized as the only group, which takes few tiles."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    rows, groups, cols = 65536, 65536, 32896
+    x = torch.randn(64, cols, generator=gen, device="cuda").to(torch.bfloat16)
+    index = torch.randint(0, 64, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    sizes = np.zeros(groups, np.int64)
+    sizes[[0, 5, 40000, 65535]] = 20001, 1, 30000, 15534
+    pad = np.concatenate([[0], np.cumsum((sizes + 127) // 128 * 128)])
+    u8 = lambda *s: torch.full(s, 0xA5, dtype=torch.uint8, device="cuda")  # noqa: E731
+    f32 = lambda *s: torch.full(s, -7.25, device="cuda")  # noqa: E731
+    q, s, qc, sc = u8(rows, cols), f32(rows, cols // 128), u8(cols, int(pad[-1])), f32(cols, int(pad[-1]) // 128)
+    fq.fp8_quantize_grouped(x, offsets(sizes), E4, row_index=index, q_row=q, s_row=s, q_col=qc, s_col=sc)
+    first = np.concatenate([[0], np.cumsum(sizes)])
+    for e in (0, 5, 40000, 65535):
+        lo, hi, p0, p1 = int(first[e]), int(first[e + 1]), int(pad[e]), int(pad[e + 1])
+        wq, ws = u8(hi - lo, cols), f32(hi - lo, cols // 128)
+        wqc, wsc = u8(cols, p1 - p0), f32(cols, (p1 - p0) // 128)
+        fq.fp8_quantize_grouped(x, offsets([hi - lo]), E4, row_index=index[lo:hi].clone(), q_row=wq, s_row=ws,
+                                q_col=wqc, s_col=wsc)
+        assert torch.equal(q[lo:hi], wq) and torch.equal(s[lo:hi], ws), e
+        assert torch.equal(qc[:, p0:p1], wqc) and torch.equal(sc[:, p0 // 128:p1 // 128], wsc), e
