@@ -1203,7 +1203,8 @@ static int fp8_grouped_gemm_impl(const uint8_t *A, int32_t fa, const float *sA, 
     if (N % 128 || K % 128) return fail(FP8Q_EUNSUPPORTED, "%s: N and K must be multiples of 128", fn);
     if (K > (int64_t)1 << 22 || N > (int64_t)1 << 23)
         return fail(FP8Q_EUNSUPPORTED, "%s: K exceeds 2^22 or N 2^23", fn);
-    if ((rows / 16 + groups) * (N / 16) > 0x7FFFFFFF) return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^31 tiles", fn);
+    if (!fp8q::grouped_gemm_fits(rows, groups, N))
+        return fail(FP8Q_EUNSUPPORTED, "%s: more tiles than one launch holds", fn);
     const void *in[5] = {A, B, sA, sB, offsets};
     const int64_t bytes[5] = {rows * K, groups * N * K, rows * (K / 128) * 4, groups * (N / 128) * (K / 128) * 4,
                               4 * ((int64_t)groups + 1)};
@@ -1237,7 +1238,8 @@ static int fp8_grouped_gemm_wgrad_impl(const uint8_t *A, int32_t fa, const float
     if (col_stride < 0 || col_stride % 128) return fail(FP8Q_EINVAL, "%s: col_stride must be a multiple of 128", fn);
     if (col_stride > (int64_t)1 << 22 || M > (int64_t)1 << 23 || N > (int64_t)1 << 23)
         return fail(FP8Q_EUNSUPPORTED, "%s: col_stride exceeds 2^22 or M or N 2^23", fn);
-    if (groups * (M / 64) * (N / 64) > 0x7FFFFFFF) return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^31 tiles", fn);
+    if (!fp8q::grouped_wgrad_fits(groups, M, N))
+        return fail(FP8Q_EUNSUPPORTED, "%s: more tiles than one launch holds", fn);
     const void *in[5] = {A, B, sA, sB, offsets};
     const int64_t bytes[5] = {M * col_stride, N * col_stride, M * (col_stride / 128) * 4, N * (col_stride / 128) * 4,
                               4 * ((int64_t)groups + 1)};

@@ -153,6 +153,10 @@ int compute_units();
 hipError_t launch_quantize_grouped(const void *x, int dtype, int64_t x_rows, int64_t cols, const int32_t *index,
                                    int64_t rows, const int32_t *offsets, int groups, int fmt, uint8_t *q_row,
                                    float *s_row, uint8_t *q_col, float *s_col, int64_t stride, hipStream_t s);
+// Whether one launch holds the tiles that any offsets could need (the largest
+// tiles' for the product, whose smaller ones give way).
+bool grouped_gemm_fits(int64_t rows, int groups, int64_t N);
+bool grouped_wgrad_fits(int groups, int64_t M, int64_t N);
 hipError_t launch_grouped_gemm(const uint8_t *A, int fa, const float *sA, const uint8_t *B, int fb, const float *sB,
                                const int32_t *offsets, int groups, int64_t rows, int64_t N, int64_t K, void *C,
                                hipStream_t s);

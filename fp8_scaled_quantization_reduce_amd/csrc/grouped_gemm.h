@@ -1021,23 +1021,34 @@ done:
 // those eight matrices 109 us against 132 us in 32 x 64 tiles, but 40 rows of
 // one 4096 x 4096 matrix 11.7 us in 32 x 32 tiles against 29 us, and in between
 // 320 rows over four 22 us in 128 x 128 tiles against 30 in the large ones.
+//
+// Tiles whose launch would pass max_blocks (16 x 32 ones of 65536 groups of one
+// row each and 8320 columns) leave the choice to larger ones; the largest fit
+// (grouped_gemm_fits).
 enum RowsTile { kRows16x16, kRows16x32, kRows32x32, kRows32x64, kRowsHalves, kRowsPP };
+
+// Waves that share a 16 x 32 tile's slices, one to four slices a wave: 64 rows
+// over eight 8192-column matrices in us with 4, 8 and 16 waves: K 1024 13.6,
+// 15.8, 18.9; 3456 44.5, 43.3, 47.0; 4096 54.4, 53.8, 52.3; 7168 88.1, 87.8, 86.6.
+inline int rows_waves(int64_t K) { return K < 2048 ? 4 : K < 4096 ? 8 : 16; }
 
 inline RowsTile rows_tile(const GroupedArgs &a)
 {
     const int64_t cus = a.cus > 0 ? a.cus : 256;
     auto blocks = [&](int tm, int tn) { return max_tiles(a.rows, a.groups, tm) * ((a.N + tn - 1) / tn); };
     const int64_t live = a.rows < a.groups ? a.rows : a.groups;
-    if (a.rows <= 12 * live) return blocks(16, 32) >= cus ? kRows16x32 : kRows16x16;
-    if (a.rows <= 18 * live && blocks(32, 64) >= cus) return kRows32x64;
-    static const struct {
-        int tm, tn;
+    const struct {
+        int tm, tn, lanes;
         double least, step;
-    } cost[6] = {{16, 16, 8.7, 5.0},   {16, 32, 8.8, 7.2},     {32, 32, 11.5, 10.5},
-                 {32, 64, 15.4, 14.5}, {128, 128, 21.0, 21.0}, {256, 256, 40.0, 40.0}};
+    } cost[6] = {{16, 16, 512, 8.7, 5.0},    {16, 32, 64 * rows_waves(a.K), 8.8, 7.2}, {32, 32, 512, 11.5, 10.5},
+                 {32, 64, 256, 15.4, 14.5}, {128, 128, 512, 21.0, 21.0},              {256, 256, 512, 40.0, 40.0}};
+    auto fits = [&](int i) { return blocks(cost[i].tm, cost[i].tn) + kXcds <= max_blocks(cost[i].lanes); };
+    if (a.rows <= 12 * live && fits(kRows16x32)) return blocks(16, 32) >= cus ? kRows16x32 : kRows16x16;
+    if (a.rows <= 18 * live && blocks(32, 64) >= cus && fits(kRows32x64)) return kRows32x64;
     RowsTile best = kRowsPP;
     double least = 0.0;
     for (int i = kRowsPP; i >= kRows16x16; --i) {
+        if (i != kRowsPP && !fits(i)) continue;
         const int64_t rounds = (blocks(cost[i].tm, cost[i].tn) + cus - 1) / cus;
         double us = cost[i].step * (double)rounds;
         if (i == kRowsPP && a.rows <= 128 * live) us *= 29.0 / 40.0; // mostly 128 x 256 tiles
@@ -1045,6 +1056,13 @@ inline RowsTile rows_tile(const GroupedArgs &a)
         if (i == kRowsPP || us < least) best = (RowsTile)i, least = us;
     }
     return best;
+}
+
+// Blocks of a launch of the large tiles on XCDs of `cus` units: with the halves
+// of what is left for a last round.
+inline int64_t pp_blocks(int64_t rows, int groups, int64_t N, int cus)
+{
+    return max_tiles(rows, groups, 256) * ((N + 255) / 256) + kXcds * (1 + cus / 2);
 }
 
 template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
@@ -1056,12 +1074,11 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
     switch (rows_tile(a)) {
     case kRows16x16: FP8Q_ROWS(1, 1, 8); break;
     case kRows16x32:
-        // one to four slices a wave: 64 rows over eight 8192-column matrices in
-        // us with 4, 8 and 16 waves: K 1024 13.6, 15.8, 18.9; 3456 44.5, 43.3,
-        // 47.0; 4096 54.4, 53.8, 52.3; 7168 88.1, 87.8, 86.6
-        if (a.K < 2048) FP8Q_ROWS(1, 2, 4);
-        else if (a.K < 4096) FP8Q_ROWS(1, 2, 8);
-        else FP8Q_ROWS(1, 2, 16);
+        switch (rows_waves(a.K)) {
+        case 4: FP8Q_ROWS(1, 2, 4); break;
+        case 8: FP8Q_ROWS(1, 2, 8); break;
+        default: FP8Q_ROWS(1, 2, 16);
+        }
         break;
     case kRows32x32: FP8Q_ROWS(2, 2, 8); break;
     case kRows32x64: FP8Q_ROWS(2, 4, 4); break;
@@ -1072,9 +1089,8 @@ template <int FA, int FB> hipError_t launch_grouped_rows(const GroupedArgs &a)
         break;
     }
     default: {
-        const int64_t tiles = max_tiles(a.rows, a.groups, 256) * ((a.N + 255) / 256);
         const int cus = a.cus / kXcds > 1 ? a.cus / kXcds : 1; // of an XCD
-        grouped_pp_kernel<FA, FB><<<(unsigned)(tiles + kXcds * (1 + cus / 2)), kBSThreads, 0, a.stream>>>(
+        grouped_pp_kernel<FA, FB><<<(unsigned)pp_blocks(a.rows, a.groups, a.N, cus), kBSThreads, 0, a.stream>>>(
             a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.N, (int)a.K, (uint16_t *)a.C, cus);
     }
     }
@@ -1109,12 +1125,16 @@ inline WgradTiles wgrad_tiles(const GroupedArgs &a)
     return bf16 && us_large <= us_small ? kWgradLarge : kWgradSmall;
 }
 
+// Blocks of a wgrad launch: the groups' tiles in equal shares of the XCDs.
+inline int64_t wgrad_blocks(int groups, int64_t M, int64_t N, int tile)
+{
+    const int64_t per = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
+    return groups * (int64_t)kXcds * ((per + kXcds - 1) / kXcds);
+}
+
 template <int FA, int FB> hipError_t launch_grouped_wgrad(const GroupedArgs &a)
 {
-    auto grid = [&](int tile) {
-        const int64_t per = ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile);
-        return (unsigned)(a.groups * (int64_t)kXcds * ((per + kXcds - 1) / kXcds));
-    };
+    auto grid = [&](int tile) { return (unsigned)wgrad_blocks(a.groups, a.M, a.N, tile); };
     const bool bf16 = a.c_dtype == kBF16;
 #define FP8Q_WGRAD(TILE, THREADS, K)                                                                                 \
     K<<<grid(TILE), THREADS, 0, a.stream>>>(a.A, a.sA, a.B, a.sB, a.offsets, a.groups, a.rows, (int)a.M, (int)a.N,  \

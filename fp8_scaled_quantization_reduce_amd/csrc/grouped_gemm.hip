@@ -13,6 +13,18 @@ FP8Q_DECLARE(e4m3_e5m2)
 FP8Q_DECLARE(e5m2_e5m2)
 #undef FP8Q_DECLARE
 
+bool grouped_gemm_fits(int64_t rows, int groups, int64_t N)
+{
+    return pp_blocks(rows, groups, N, 256) <= max_blocks(kBSThreads);
+}
+
+// 64 x 64 tiles are only taken where there are few
+bool grouped_wgrad_fits(int groups, int64_t M, int64_t N)
+{
+    return wgrad_blocks(groups, M, N, 128) <= max_blocks(256) &&
+           wgrad_blocks(groups, M, N, 256) <= max_blocks(kBSThreads);
+}
+
 hipError_t launch_grouped_gemm(const uint8_t *A, int fa, const float *sA, const uint8_t *B, int fb, const float *sB,
                                const int32_t *offsets, int groups, int64_t rows, int64_t N, int64_t K, void *C,
                                hipStream_t s)

@@ -482,7 +482,8 @@ int fp8_quantize_grouped(const void *x, int32_t dtype, int64_t x_rows, int64_t c
  *   C  [rows][N] bf16
  * with the arithmetic of fp8_scaled_gemm(FP8Q_BLOCK_1x128_128x128).  Groups
  * may have any number of rows; N and K are multiples of 128 (K at most 2^22,
- * N at most 2^23).
+ * N at most 2^23).  256x256 tiles of all rows and groups, a part of one counted
+ * as whole, are at most 2^23 - 1100.
  */
 int fp8_grouped_gemm(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb, const float *sB,
                      const int32_t *offsets, int32_t groups, int64_t rows, int64_t N, int64_t K, void *C,
@@ -503,7 +504,9 @@ int fp8_grouped_gemm(const uint8_t *A, int32_t fa, const float *sA, const uint8_
  * widened to bf16 (exactly) for the bf16 matrix instruction, whose sums are
  * binary32: the FP8 instruction adds neighbouring products on about 15 bits,
  * which an fp32 gradient would show (1.1e-5 in the 2-norm).
- * M and N are multiples of 128 and at most 2^23, col_stride at most 2^22.
+ * M and N are multiples of 128 and at most 2^23, col_stride at most 2^22, and the
+ * 128x128 tiles of a gradient, rounded up to a multiple of 8, times the groups
+ * less than 2^24 (256x256 tiles 2^23).
  */
 int fp8_grouped_gemm_wgrad(const uint8_t *A, int32_t fa, const float *sA, const uint8_t *B, int32_t fb,
                            const float *sB, const int32_t *offsets, int32_t groups, int64_t rows, int64_t col_stride,

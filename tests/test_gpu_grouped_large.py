@@ -292,3 +292,30 @@ def test_quantize_more_tiles_than_one_launch_holds():
                                 q_col=wqc, s_col=wsc)
         assert torch.equal(q[lo:hi], wq) and torch.equal(s[lo:hi], ws), e
         assert torch.equal(qc[:, p0:p1], wqc) and torch.equal(sc[:, p0 // 128:p1 // 128], wsc), e
+
+
+def test_gemm_more_small_tiles_than_one_launch_holds():
+    """One row a group on average over 65536 groups: the 16-row tiles that few
+    rows take would be more than 2^32 lanes.  Only groups with rows have weights
+    written; the others' are never read."""
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    rows, groups, n, k = 65536, 65536, 8320, 128
+    sizes = np.zeros(groups, np.int64)
+    live = [0, 5, 40000, 65535]
+    sizes[live] = 20001, 1, 30000, 15534
+    a, sa, sb = codes(gen, rows, k), scales(gen, rows, 1), scales(gen, groups, n // 128, 1)
+    b = torch.empty(groups, n, k, dtype=torch.uint8, device="cuda")
+    for e in live:
+        b[e] = codes(gen, n, k)
+    c = torch.full((rows, n), 777.0, dtype=torch.bfloat16, device="cuda")
+    fq.fp8_grouped_gemm(a, E4, sa, b, E4, sb, offsets(sizes), c)
+    col = np.concatenate([np.arange(0, n, 129), [n - 1]])
+    first = np.concatenate([[0], np.cumsum(sizes)])
+    for e in live:
+        lo, hi = int(first[e]), int(first[e + 1])
+        t = np.unique(np.concatenate([np.arange(lo, hi, 1009), [hi - 1]]))
+        wa = value(a[torch.from_numpy(t).cuda()], E4) * host(sa)[t].astype(np.float64)
+        wb = value(b[e][torch.from_numpy(col).cuda()], E4) * host(sb[e])[col // 128].astype(np.float64)
+        close(c[torch.from_numpy(t).cuda()][:, torch.from_numpy(col).cuda()], wa, wb, k)
+    del b, c
+    torch.cuda.empty_cache()  # 70 GB that no other test takes

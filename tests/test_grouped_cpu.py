@@ -147,3 +147,11 @@ def test_quantize_grouped_without_rows_does_nothing():
     _expect(_q(rows=0, dt=2), fq.EINVAL, "dtype")
     _expect(_q(rows=0, off=None), fq.EINVAL, "offsets")
     _expect(_q(rows=0, stride=500), fq.EINVAL, "col_stride")
+
+
+def test_more_tiles_than_one_launch_holds():
+    """Refused on the host: a launch of 2^32 lanes or more would be cut off."""
+    _expect(_g(rows=1 << 16, groups=1 << 16, N=1 << 15, K=128), fq.EUNSUPPORTED, "one launch")
+    _expect(_g(rows=1 << 26, groups=1, N=1 << 13, K=128), fq.EUNSUPPORTED, "one launch")
+    _expect(_w(groups=1, M=1 << 20, N=1 << 19), fq.EUNSUPPORTED, "one launch")
+    _expect(_w(groups=1 << 16, M=1 << 12, N=1 << 10), fq.EUNSUPPORTED, "one launch")
