@@ -944,6 +944,9 @@ static int layernorm_shape(const char *fn, int32_t dtype, int64_t rows, int64_t 
     if (rows < 0 || cols < 1) return fail(FP8Q_EINVAL, "%s: rows must be >= 0 and cols >= 1", fn);
     if (rows > (int64_t)1 << 31 || cols > (int64_t)1 << 31)
         return fail(FP8Q_EUNSUPPORTED, "%s: a dimension exceeds 2^31", fn);
+    // keeps the buffers' sizes, which the overlap checks compare, in 64 bits
+    if (rows > 0 && cols > ((int64_t)1 << 40) / rows)
+        return fail(FP8Q_EUNSUPPORTED, "%s: more than 2^40 elements", fn);
     return FP8Q_OK;
 }
 

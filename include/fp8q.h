@@ -518,8 +518,8 @@ int fp8_grouped_gemm_wgrad(const uint8_t *A, int32_t fa, const float *sA, const 
  *   mean = sum_j x_j / cols, var = sum_j (x_j - mean)^2 / cols,
  *   rstd = 1 / sqrt(var + eps), y_j = (x_j - mean) rstd gamma_j + beta_j
  * in binary32, y rounded once to its type.
- *   x, y    [rows][cols] of `dtype` (FP8Q_F32 or FP8Q_BF16); any sizes,
- *           cols >= 1; aligned to their elements (16 bytes is not needed here
+ *   x, y    [rows][cols] of `dtype` (FP8Q_F32 or FP8Q_BF16); any sizes up to
+ *           2^31 rows, 2^31 columns and 2^40 elements, cols >= 1; aligned to their elements (16 bytes is not needed here
  *           and in the two calls below)
  *   gamma, beta (nullable: ones, zeros)  [cols] of `p_dtype`
  *   eps     finite, not negative

@@ -132,3 +132,14 @@ def test_binding_refuses(i):
     call, exc, fragment = BAD_CALLS[i]
     with pytest.raises(exc, match=fragment):
         call()
+
+
+def test_layernorm_sizes_whose_bytes_pass_64_bits():
+    """2^64 bytes would look like none to the overlap checks (here y on x, dx on x)."""
+    big = 1 << 31
+    _expect(_ln(dtype=fq.F32, rows=big, cols=big, y=BAD), fq.EUNSUPPORTED, "2^40")
+    _expect(_ln(rows=(1 << 20) + 1, cols=1 << 20), fq.EUNSUPPORTED, "2^40")
+    _expect(_lnb(dtype=fq.F32, rows=big, cols=big, dx=BAD + 0x10000), fq.EUNSUPPORTED, "2^40")
+    n = ctypes.c_int64(-1)
+    _expect(L.fp8q_layernorm_backward_workspace(0, big, big, ctypes.byref(n)), fq.EUNSUPPORTED, "2^40")
+    assert L.fp8q_layernorm_backward_workspace(0, 1 << 20, 1 << 20, ctypes.byref(n)) == fq.OK and n.value > 0
