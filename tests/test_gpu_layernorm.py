@@ -244,3 +244,15 @@ def test_backward_of_more_columns_than_one_launch_of_the_fold_has_lanes():
     # x - mean, its product with rstd (exact here but for one rounding each) and with dy
     assert torch.all((dg[:cols].double() - want).abs() <= 4 * U * want.abs())
     assert torch.all(dg[cols:] == 777.0) and torch.all(db[cols:] == 777.0)
+
+
+# the register shapes that SHAPES leaves out: whole rows of vectors (256, 6144,
+# 12288, 16384 columns) and rows that end inside one
+@pytest.mark.parametrize("cols", [256, 2500, 3500, 6144, 7001, 10007, 12288, 16384, 20001])
+@pytest.mark.parametrize("dt,pt", [("bf16", "f32"), ("f32", "bf16")])
+def test_remaining_register_shapes(cols, dt, pt):
+    # more rows than the backward pass has blocks, so that a row ahead is fetched
+    rows = 1100
+    x, gamma, beta, dy = draw(rows, cols, dt, pt, cols)
+    check_forward(x, gamma, beta, 1e-5, dt)
+    check_backward(x, dy, gamma, dt, pt)
