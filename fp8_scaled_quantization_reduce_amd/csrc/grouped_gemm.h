@@ -688,12 +688,15 @@ __device__ __forceinline__ bool wgrad_tile(const uint8_t *A, const float *sA, co
 // stage is free for the slice after next while the products run.
 //
 // Eight 14336 x 4096 gradients over 8192 tokens, fp32: 1.15 ms, 0.84 PFLOP/s,
-// 1.9 GB written.  The chip's power bounds it: in 256 x 128 ping-pong tiles of
-// one block per CU the same work took 30% more cycles at a 25% higher clock
-// (2.91 million at 2.25 GHz, here 2.23 at 1.78).  Without the loads of the
-// slices it would take 15% less time, without the widening 11%, without the
-// scales 9%.  Eight 4096 x 4096 over 1024 tokens, where the stores count: 113
-// us against 146.
+// 1.9 GB written, 2.08 million cycles at the 1.83 GHz that the card's power leaves.
+// A library's bf16 product of as many operations, one 14336 x 4096 gradient over
+// 8192 tokens, takes 0.75 ms at 1.97 GHz (1.48 million cycles), so power is a
+// part of the distance; the rest is work beside the products.  Without the loads
+// of the slices the kernel takes 15% less time, without the widening (two waves
+// widen every code) 11%, without the scales 9%; a tile also has a fixed cost
+// (finding the group, first loads, stores).  256 x 128 ping-pong tiles of one
+// block per CU took 3% longer, with 30% more cycles at a higher clock.  Eight
+// 4096 x 4096 over 1024 tokens, where the stores count: 113 us against 146.
 template <int FA, int FB, int DC>
 __global__ __launch_bounds__(256, 2) void grouped_wgrad_kernel(
     const uint8_t *__restrict__ A, const float *__restrict__ sA, const uint8_t *__restrict__ B,

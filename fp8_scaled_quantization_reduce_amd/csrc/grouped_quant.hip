@@ -19,8 +19,9 @@
 // Both are bound by memory, and both store with the non-temporal hint, which
 // leaves the caches to rows that several experts read: 8192 rows of 4096 bf16
 // to two experts each, both copies 46 us (5.8 TB/s of what moves; 63 us with
-// ordinary row stores), rows alone 32 us (39).  A block that walked several
-// column tiles with the next one fetched ahead spilled: 8% slower.
+// ordinary row stores), rows alone 32 us (39); fp32 with both copies 58 us.  A
+// block that walked several column tiles with the next one fetched ahead
+// spilled: 8% slower.
 #include "fp8q_device.h"
 #include "fp8q_launch.h"
 #include "groups.h"
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(kGqThreads, 4) void tile_both_kernel(
     __shared__ __attribute__((aligned(16))) uint32_t tl[128 * 32]; // column codes, [column][row / 4]
     __shared__ uint32_t colmax[4][128 / kPer];
     __shared__ float colscale[128];
-    __shared__ uint32_t colbad; // some column scale is NaN, infinite or zero
+    __shared__ uint32_t colbad; // some column's maximum is NaN or infinite (no scale is zero: amax has a floor)
     const int blocks_c = (int)(cols / 128);
     const int t = t0 + (int)(blockIdx.x / blocks_c), cb = (int)(blockIdx.x % blocks_c);
     GroupTiles<128> tiles(offsets, groups, rows);

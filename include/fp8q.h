@@ -565,7 +565,9 @@ int fp8q_layernorm_backward_workspace(int32_t dtype, int64_t rows, int64_t cols,
  *   g      HOST array of `count` device pointers; tensor i has n[i] >= 0
  *          elements of dtype[i] (host arrays too), aligned to its elements
  *   out    HOST array of device pointers of the same sizes and types, each
- *          equal to g[i] or overlapping no gradient; NULL: in place
+ *          equal to g[i] or overlapping no gradient, and no two overlapping;
+ *          NULL: in place.  A gradient that is written in place may not
+ *          overlap another (so may not be listed twice)
  *   max_norm  not negative; +inf: only the norm is computed, coef is 1 (also
  *          with an infinite norm; NaN with a NaN norm) and out must be NULL
  *   norm, coef  one device float each
