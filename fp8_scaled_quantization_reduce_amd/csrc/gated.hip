@@ -70,17 +70,11 @@ __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t to, int dtype, int
 constexpr int kFinishThreads = 256;
 
 __global__ __launch_bounds__(kFinishThreads) void gated_finish_kernel(const int32_t *__restrict__ offsets, int groups,
-                                                                      int rows, int F, GatedOut o)
+                                                                      int rows, int tiles, int F, GatedOut o)
 {
-    int lo = 0, hi = rows; // the groups' rows, looked up beside the loads of the values
-    if (offsets) {
-        lo = min(max(offsets[0], 0), rows);
-        hi = min(max(offsets[groups], 0), rows);
-    }
     const int lane = threadIdx.x & 63, blocks = F / 128;
     const int64_t i = (int64_t)blockIdx.x * (kFinishThreads / 16) + (threadIdx.x >> 4);
     const int64_t row = i / blocks, b = i % blocks;
-    const bool live = row >= lo && row < hi; // of a group (16 lanes agree); other rows are read, not written
     const int64_t c = b * 128 + 8 * (lane & 15);
     float g[8], u[8], h[8];
 #pragma unroll
@@ -94,6 +88,8 @@ __global__ __launch_bounds__(kFinishThreads) void gated_finish_kernel(const int3
             for (int e = 0; e < 4; ++e) g[4 * k + e] = x[e], u[4 * k + e] = y[e];
         }
     }
+    // rows that the product's tiles filled, looked up beside the loads of the values
+    const bool live = offsets ? row_in_tiles<16>(offsets, groups, rows, tiles, (int)row) : row < rows;
     with_act(o.act, [&](auto a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[e] = act_f32<decltype(a)::value>(g[e]) * u[e];
@@ -538,8 +534,8 @@ hipError_t launch_gated_gemm(const uint8_t *A, int fa, const float *sA, const ui
                     : (fb == kE4M3 ? launch_gated_e5m2_e4m3(a) : launch_gated_e5m2_e5m2(a));
     if (e != hipSuccess || !ws) return e;
     const int64_t units = rows * (F / 128), per = kFinishThreads / 16;
-    gated_finish_kernel<<<(unsigned)((units + per - 1) / per), kFinishThreads, 0, s>>>(offsets, groups, (int)rows, (int)F,
-                                                                                     out);
+    gated_finish_kernel<<<(unsigned)((units + per - 1) / per), kFinishThreads, 0, s>>>(
+        offsets, groups, (int)rows, (int)max_tiles(rows, groups, 16), (int)F, out);
     return hipGetLastError();
 }
 

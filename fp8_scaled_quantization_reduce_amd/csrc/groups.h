@@ -95,6 +95,29 @@ template <int kTile> struct GroupTiles {
     }
 };
 
+// Whether a launch of GroupTiles<kTile> that covers its first `launched` tiles has
+// the row of a lane's 16 lanes in one of them; for a pass over rows behind such a
+// launch.  Offsets that decrease leave gaps, and tiles past the launch, so the
+// groups' ends alone do not say it.  All 64 lanes must call it.
+template <int kTile>
+__device__ __forceinline__ bool row_in_tiles(const int32_t *offsets, int groups, int rows, int launched, int row)
+{
+    const int lane = threadIdx.x & 63, most = min(launched, rows / kTile + groups);
+    unsigned found = 0; // bit k: of lanes 16 k .. 16 k + 15
+    for (int g0 = 0, base = 0; g0 < groups && base < most && found != 15; g0 += 64) {
+        int lo, size;
+        group_rows(offsets, groups, rows, g0 + lane, lo, size);
+        const int count = (int)(((unsigned)size + kTile - 1) / kTile), sum = wave_scan_i32(count);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int in = __builtin_amdgcn_readlane(row, 16 * k) - lo;
+            if (__ballot((unsigned)in < (unsigned)size && base + sum - count + in / kTile < most)) found |= 1u << k;
+        }
+        base += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return found >> (lane >> 4) & 1;
+}
+
 // The most tiles of `tile` rows that `groups` groups over `rows` rows can
 // have: sum ceil(m / tile) over at most min(groups, rows) groups with rows.
 inline int64_t max_tiles(int64_t rows, int groups, int tile)
