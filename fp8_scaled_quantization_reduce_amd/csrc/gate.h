@@ -9,8 +9,11 @@ namespace fp8q {
 
 constexpr int kActSilu = 3; // beside Act; only the gated calls take it
 
-// 1 / (1 + e^-x) with one exp2 and one reciprocal (1 ulp each).  0 below -88,
-// where e^-x leaves binary32, 1 at +inf.
+// 1 / (1 + e^-x) with one exp2 and one reciprocal (1 ulp each).  The exponent's one
+// rounding and the constant's are worth 1.22 |x| 2^-24 of e^-x, so of the result where
+// x is negative (12 x 2^-24 at -10); bringing that to a few 2^-24 takes four
+// operations more, an eighth of the backward pass's arithmetic, for results that 8-bit
+// codes hold to 2^-4.  0 below -88, where e^-x leaves binary32, 1 at +inf.
 __device__ __forceinline__ float sigmoid_f32(float x)
 {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
@@ -18,7 +21,7 @@ __device__ __forceinline__ float sigmoid_f32(float x)
 
 // act(x) and act'(x).
 //   ReLU: x < 0 -> 0, NaN kept; the derivative at 0 is 0, at NaN NaN
-//   GELU: x Phi(x); Phi(x) + x phi(x)
+//   GELU: x Phi(x); Phi(x) + x phi(x) (Phi within 2^-21, phi's exponent rounded as above)
 //   SiLU: x p with p = sigmoid(x); p (1 + x (1 - p))
 // GELU and SiLU are NaN at -inf (-inf times 0).
 template <int ACT> __device__ __forceinline__ float act_f32(float x)

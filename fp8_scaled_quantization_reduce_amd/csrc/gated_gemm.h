@@ -5,7 +5,11 @@
 //   g[t] = sum over slices kb of fma(part_kb, fl32(sA[t, kb] sB[e, n / 128, kb]), .)
 //   u[t] likewise with the rows F .. 2F - 1 of B_e,  h[t, n] = act(g) u
 //
-// in the arithmetic of the grouped product.  A 1x128 block of h needs 128
+// in the arithmetic of the grouped product, part_kb on the FP8 matrix instruction,
+// whose narrow adder leaves g and u 1.4e-5 to 2e-5 off in the 2-norm.  A binary32 h
+// shows that; bf16 (1.7e-3) hides it, and of the codes one in a thousand falls on the
+// other side of its rounding, 1.4e-3 in their 2-norm beside the format's 2.6e-2.  That
+// is taken for twice the rate of the bf16 instruction on widened codes.  A 1x128 block of h needs 128
 // columns of g and of u in one place: the large tiles hold 256, 128 or 64 rows x
 // 128 columns of h, so a block's codes leave with the tile.  The tiles for few
 // rows hold 16 columns, as many blocks as it takes to read the weights at the
@@ -224,8 +228,10 @@ __global__ __launch_bounds__(kBSThreads, 1) void gated_pp_kernel(const uint8_t *
 // what bounds K (kMidSlices).
 //
 // What the LDS moves bounds a slice, 96 KB read and 40 KB written, 0.5 us: 301 rows
-// of 4096 x 4096 24 us on 160 CUs, 20 of it the 32 slices of a tile; many weights,
-// their bytes: 32 rows of each of 64 matrices of 1408 x 2048 73 us, 5.1 TB/s.
+// of 4096 x 4096 24 us on 160 CUs, 20 of it the 32 slices of a tile, with the weights in
+// the last-level cache; from memory 28, and 0.85 us a slice where 32 CUs read all
+// of them.  Many weights, their bytes: 32 rows of each of 64 matrices of 1408 x 2048
+// 73 to 79 us, 5.1 TB/s.
 // Weights straight from memory into registers took 1 us a slice (every load
 // touches half a line of 16 rows), four waves of 64 x (32 + 32), which read a third
 // less from LDS, 0.7 us (one wave a SIMD waits for its own reads).

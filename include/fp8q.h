@@ -521,8 +521,9 @@ int fp8_grouped_gemm_wgrad(const uint8_t *A, int32_t fa, const float *sA, const 
  * in outputs indexed by row, and with no rows, groups or columns a call does
  * nothing and the buffers, which are empty, may be null.
  *   act: FP8Q_ACT_SILU (x / (1 + e^-x)), FP8Q_ACT_GELU (the exact form, as in
- *   fp8_scaled_gemm_fused) or FP8Q_ACT_RELU; evaluated in binary32.  SiLU and
- *   GELU of -inf are NaN.
+ *   fp8_scaled_gemm_fused) or FP8Q_ACT_RELU; evaluated in binary32, SiLU to
+ *   (1.22 |g| + 6) 2^-24 of its value, GELU to 2^-21 |g|.  SiLU and GELU of -inf
+ *   are NaN.
  *
  * fp8_gated_gemm -- both projections, the activation and the product:
  *   g[t] = (A[t] * sA[t]) (Bg_e * sBg_e)^T, u[t] with Bu_e, h = act(g) u
@@ -536,7 +537,9 @@ int fp8_grouped_gemm_wgrad(const uint8_t *A, int32_t fa, const float *sA, const 
  *   q_gu, s_gu  (nullable, together) [g u] in 1x128 blocks, codes [rows][2F] of
  *      gu_fmt and scales [rows][2F/128]: the checkpoint for fp8_gated_backward
  *   At least one of the three.  g and u have the arithmetic of
- *   fp8_grouped_gemm before its rounding; h and the blocks are formed from their
+ *   fp8_grouped_gemm before its rounding, on the FP8 matrix instruction whatever
+ *   the outputs (1.4e-5 to 2e-5 off in the 2-norm: an FP8Q_F32 H shows it, unlike
+ *   fp8_grouped_gemm_wgrad's FP8Q_F32 gradients); h and the blocks are formed from their
  *   binary32 values, the blocks as fp8_quantize_block (block_rows 1) forms them.
  *   workspace  16-byte aligned device memory of at least the bytes that
  *      fp8_gated_gemm_workspace gives for these sizes, contents free to be
