@@ -80,3 +80,38 @@ def test_long_contractions(k):
         assert bool(((c.double() - want).abs() <= tol).all())
         check_rows(host(q_gu[lo:hi]), host(s_gu[lo:hi]), host(c), E4)
         assert torch.equal(H[lo:hi], torch.where(c[:, :F] < 0, 0.0, c[:, :F]) * c[:, F:])
+
+
+@pytest.mark.parametrize("rows", [3, 4100])  # 16-row tiles, and the large ones
+def test_the_longest_contraction(rows):
+    """K = 2^22, 32768 slices: rows at both ends against fp8_scaled_gemm, whose order of
+    the slices' sums the large tiles have; the 16-row ones add 16 waves' instead, each
+    order within 32768 2^-24 of the sum S of the slices' magnitudes."""
+    F, K, gen = 128, 1 << 22, torch.Generator(device="cuda").manual_seed(rows)
+    assert (fq.fp8_gated_gemm_workspace(rows, 1, F, K) > 0) == (rows == 3)
+    a, sa, b, sb = codes(gen, rows, K), scales(gen, rows, K // 128), codes(gen, 2 * F, K), scales(gen, 2, K // 128)
+    size = fq.fp8_gated_gemm_workspace(rows, 1, F, K)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
+    q_gu, s_gu = torch.empty(rows, 2 * F, dtype=torch.uint8, device="cuda"), torch.empty(rows, 2, device="cuda")
+    fq.fp8_gated_gemm(a, E4, sa, b, E4, sb, RELU, q_gu=q_gu, s_gu=s_gu, workspace=ws)
+    for lo, hi in {(0, min(rows, 128)), (max(0, rows - 128), rows)}:
+        pa, ps = torch.zeros(128, K, dtype=torch.uint8, device="cuda"), torch.ones(128, K // 128, device="cuda")
+        pa[:hi - lo], ps[:hi - lo] = a[lo:hi], sa[lo:hi]
+        c = torch.empty(128, 2 * F, device="cuda")
+        fq.fp8_scaled_gemm(pa, E4, ps, b, E4, sb, fq.BLOCK_1x128_128x128, c)
+        c = c[:hi - lo].contiguous()
+        assert bool(torch.isfinite(c).all())
+        if rows > 3:
+            check_rows(host(q_gu[lo:hi]), host(s_gu[lo:hi]), host(c), E4)
+            continue
+        most = torch.zeros(hi - lo, 2 * F, dtype=torch.float64, device="cuda")  # a slice's part is at most its products'
+        for k in range(0, K, 1 << 18):
+            x = a[lo:hi, k:k + (1 << 18)].view(torch.float8_e4m3fn).float().double().abs()
+            x *= sa[lo:hi, k // 128:k // 128 + 2048].double().repeat_interleave(128, 1)
+            w = b[:, k:k + (1 << 18)].view(torch.float8_e4m3fn).float().double().abs()
+            w *= sb[:, k // 128:k // 128 + 2048].double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+            most += x @ w.t()
+        each = s_gu.double().repeat_interleave(128, 1)
+        off = (q_gu.view(torch.float8_e4m3fn).float().double() * each - c.double()).abs()
+        tol = 2 * 32768 * U * most
+        assert bool((off <= tol + 2.0 ** -4 * (c.double().abs() + tol) + 2.0 ** -10 * each).all())
